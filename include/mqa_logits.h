@@ -68,6 +68,9 @@ typedef enum mqa_status {
                                          tiles, or an mbarrier that ended in another phase than
                                          its use count predicts. The output is still written. */
 
+#define MQA_STATUS_NO_PAGES     0x40u /* mqa_pages_resize: too few free pages; rows that did not fit
+                                         kept their length */
+
 /* mqa_logits_params.flags */
 #define MQA_FLAG_VALIDATE 0x1u   /* device-side checks (also enabled by env MQA_LOGITS_VALIDATE=1) */
 #define MQA_FLAG_NO_PDL   0x2u   /* launch without programmatic dependent launch */

@@ -11,7 +11,9 @@ the calls raise.
     idx = mqa_logits_topk(out, context_lens, k, by_token=True)
 
 mqa_logits_topk_merge merges per-shard top-k lists of a row split over GPUs
-by token range (shard.sharded_topk does the exchange). PyTorch is used for
+by token range (shard.sharded_topk does the exchange). The calls around the
+cache (appends, attention over the FP4 cache, pages; include/mqa_cache.h) are in
+cache.py and named here. PyTorch is used for
 device memory and streams only.
 """
 from __future__ import annotations
@@ -23,6 +25,11 @@ from typing import Optional
 
 import torch
 
+from .cache import (MQA_PAGES_MAX_CACHES, AppendParams, AttentionParams, PagesParams, declare as
+                    _declare_cache, mqa_attention_workspace, mqa_cache_append_fp4,
+                    mqa_cache_append_fp8, mqa_pages_compact, mqa_pages_copy, mqa_pages_fork,
+                    mqa_pages_resize, paged_mqa_attention_fp4)
+
 __all__ = [
     "MQALogitsError", "Params", "library", "library_path", "mqa_logits_num_ctas",
     "mqa_logits_schedule", "paged_mqa_logits_fp8", "paged_mqa_logits_fp4",
@@ -33,6 +40,10 @@ __all__ = [
     "MQA_TOPK_MERGE_MAX", "MQA_TOPK_MERGE_MAX_SHARDS", "MQA_FLAG_VALIDATE", "MQA_FLAG_NO_PDL",
     "MQA_STATUS_TIMEOUT", "MQA_STATUS_BAD_PAGE", "MQA_STATUS_BAD_CONTEXT",
     "MQA_STATUS_STALE_SCHEDULE", "MQA_STATUS_Q_RANGE", "MQA_STATUS_DEBUG_INVARIANT", "SCHEDULE_UNIT",
+    "MQA_STATUS_NO_PAGES", "MQA_PAGES_MAX_CACHES", "AttentionParams", "AppendParams",
+    "PagesParams", "paged_mqa_attention_fp4", "mqa_attention_workspace", "mqa_cache_append_fp8",
+    "mqa_cache_append_fp4", "mqa_pages_fork", "mqa_pages_resize", "mqa_pages_compact",
+    "mqa_pages_copy",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +67,7 @@ MQA_STATUS_BAD_CONTEXT = 0x4
 MQA_STATUS_STALE_SCHEDULE = 0x8
 MQA_STATUS_Q_RANGE = 0x10
 MQA_STATUS_DEBUG_INVARIANT = 0x20
+MQA_STATUS_NO_PAGES = 0x40
 SCHEDULE_UNIT = 256
 
 _STATUS_NAMES = {0: "MQA_OK", -1: "MQA_ERR_INVALID_ARG", -2: "MQA_ERR_ARCH",
@@ -120,6 +132,7 @@ def library() -> ctypes.CDLL:
             L.mqa_logits_last_error.argtypes = []
             L.mqa_logits_version.restype = ctypes.c_char_p
             L.mqa_logits_version.argtypes = []
+            _declare_cache(L)
             _lib = L
     return _lib
 

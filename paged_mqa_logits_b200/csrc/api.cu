@@ -12,6 +12,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "mqa_logits_diag.h"
 
 namespace mqa {
@@ -31,7 +32,6 @@ int launch_topk_merge(const float* cand_values, const int32_t* cand_tokens, int 
                       float* values, void* stream);
 
 constexpr int kMaxBatchSchedule = 32768;
-constexpr int kMaxCtas = 4096;
 constexpr int kMaxStages = 16;  // cap on the MQA_LOGITS_STAGES override
 // Default K ring depths (units of 256 tokens).
 constexpr int kDefaultStages = 3;     // FP4 kernels (three producer warps)
@@ -43,8 +43,8 @@ constexpr int kDefaultStagesFp8 = 5;  // FP8 kernel (one producer, units issued 
 __device__ uint32_t g_lib_status;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -60,12 +60,9 @@ int cuda_fail(cudaError_t e, const char* what) {
     return fail(MQA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-
 // Compute capability 10.0 check, cached per device; on the first success on
 // a device it also looks up that device's copy of g_lib_status.
-int check_arch(int* device_out, uint32_t** lib_status = nullptr) {
+int check_arch(int* device_out, uint32_t** lib_status) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -98,6 +95,13 @@ int check_arch(int* device_out, uint32_t** lib_status = nullptr) {
     if (device_out) *device_out = dev;
     return MQA_OK;
 }
+
+bool env_flag(const char* name) {
+    const char* v = std::getenv(name);
+    return v && v[0] && std::strcmp(v, "0") != 0;
+}
+
+namespace {
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -145,11 +149,6 @@ int max_optin_smem(int dev, int* out) {
     cudaError_t e = cudaDeviceGetAttribute(out, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute(smem)");
     return MQA_OK;
-}
-
-bool env_flag(const char* name) {
-    const char* v = std::getenv(name);
-    return v && v[0] && std::strcmp(v, "0") != 0;
 }
 
 int env_int(const char* name, int dflt) {
@@ -511,11 +510,11 @@ int mqa_logits_check_status(void* stream) {
     if (rc != MQA_OK) return rc;
     if (v == 0) return MQA_OK;
     static const char* const names[] = {"TIMEOUT", "BAD_PAGE", "BAD_CONTEXT", "STALE_SCHEDULE",
-                                        "Q_RANGE", "DEBUG_INVARIANT"};
+                                        "Q_RANGE", "DEBUG_INVARIANT", "NO_PAGES"};
     std::string msg;
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 7; ++i)
         if (v & (1u << i)) msg += std::string(" ") + names[i];
-    if (v >> 6) msg += " (unknown bits)";
+    if (v >> 7) msg += " (unknown bits)";
     return fail(MQA_ERR_DEVICE_CHECK, "device status 0x%x:%s", v, msg.c_str());
 }
 

@@ -1,0 +1,51 @@
+// Arguments and the split rule of the attention kernels (attention.cu).
+#pragma once
+#include <cuda_runtime.h>
+
+#include "cache.cuh"
+
+namespace mqa {
+
+struct AttentionArgs {
+    const void* q;
+    const uint8_t* k;
+    const uint8_t* v;
+    const int32_t* block_table;
+    const int32_t* context_lens;
+    const int32_t* schedule;  // dense
+    const int32_t* indices;   // selected tokens
+    void* out;
+    float* lse;               // may be NULL
+    float* part_o;            // [slots][Hk][rows][D]
+    float* part_ml;           // [slots][Hk][rows][4]: maximum, sum, sum of unrounded p
+    int64_t q_sb, q_sn, q_sh; // strides of q in elements
+    int64_t page_bytes;       // of one cache: Hk heads
+    StatusWords status;
+    float scale_log2;         // softmax_scale * log2(e)
+    int32_t batch, next_n, heads, kv_heads, group;
+    int32_t rows;             // query rows of one work item and kv head: group * next_n, or group (selected)
+    int32_t page_size, ps_shift, num_pages, max_pages;
+    int32_t num_ctas;         // dense: S
+    int32_t topk, splits;     // selected: list length, CTAs per list
+};
+
+// CTAs that share one list of `topk` tokens: enough for two CTAs on every SM,
+// at most one per 256 entries (a CTA's 8 warps take 32 tokens each at a time).
+inline int topk_splits(int64_t lists, int topk, int sms) {
+    int64_t s = (2 * (int64_t)sms + lists - 1) / lists;
+    const int64_t most = (topk + 255) / 256;
+    if (s > most) s = most;
+    return s < 1 ? 1 : (int)s;
+}
+
+// Slots of partial results: dense, two per CTA of the schedule (the row it
+// starts inside of, the row it ends inside of); selected, one per CTA.
+inline int64_t attention_slots(const AttentionArgs& a) {
+    if (a.topk == 0) return 2 * (int64_t)a.num_ctas;
+    return a.splits > 1 ? (int64_t)a.batch * a.next_n * a.splits : 0;
+}
+
+cudaError_t launch_attention(int device, int head_dim, int dtype, const AttentionArgs& a,
+                             void* stream, bool pdl);
+
+}  // namespace mqa

@@ -1,0 +1,356 @@
+// Page tables and reference counts: fork, resize, compact; and the copy of pages.
+//
+// Every decision is a function of the tables, lengths and counts alone: free
+// pages are ranked by number (prefix sums over page_refs), rows by index, and
+// the atomics on page_refs only add, so no result depends on thread order.
+#include "pages.cuh"
+
+#include "host.cuh"
+
+namespace mqa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPer = 8;                           // page counts per thread and round of a scan
+constexpr int kRound = kPlanThreads * kPer;
+
+// Exclusive prefix sum over the CTA (kPlanThreads threads); `total` gets the sum.
+// `tmp` holds 33 ints of shared memory; all threads call.
+__device__ __forceinline__ int block_scan(int v, int* tmp, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = tmp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        tmp[lane] = s;
+    }
+    __syncthreads();
+    total = tmp[31];
+    const int before = (warp ? tmp[warp - 1] : 0) + x - v;
+    __syncthreads();
+    return before;
+}
+
+// The page counts [first, first + kPer) (1 behind the pool: neither free nor, for
+// compact, looked at).
+__device__ __forceinline__ void load_refs(const int32_t* refs, int first, int num, int (&r)[kPer]) {
+    if (first + kPer <= num && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < kPer; i += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(refs + first + i);
+            r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) r[i] = first + i < num ? refs[first + i] : 1;
+    }
+}
+
+__device__ __forceinline__ int pages_of(const PagesArgs& a, int len) {
+    return (int)(((int64_t)len + a.page_size - 1) >> a.ps_shift);
+}
+
+__device__ __forceinline__ int len_of(const PagesArgs& a, const int32_t* lens, int b) {
+    return clamp_len(a.status, lens[b], a.max_pages << a.ps_shift);
+}
+
+__device__ __forceinline__ bool good_page(const PagesArgs& a, int p) {
+    if (p >= 0 && p < a.num_pages) return true;
+    report_checked(a.status, MQA_STATUS_BAD_PAGE);
+    return false;
+}
+
+// ---------------------------------------------------------------- fork
+// CTA x takes old row x's references off and writes new row x with its own on; a
+// row that goes on from itself keeps its counts untouched.
+__global__ void __launch_bounds__(128) fork_kernel(const int32_t* table, const int32_t* lens,
+                                                   const int32_t* parents, int32_t* refs,
+                                                   int32_t* out_table, int32_t* out_lens,
+                                                   PagesArgs a) {
+    ptx::griddep_wait();
+    const int r = blockIdx.x;
+    int parent = -1;
+    if (r < a.out_batch) {
+        parent = parents[r];
+        if (parent < 0 || parent >= a.batch) {
+            if (parent != -1 && threadIdx.x == 0) report_checked(a.status, MQA_STATUS_BAD_CONTEXT);
+            parent = -1;
+        }
+    }
+    if (r < a.batch && parent != r) {
+        const int n = pages_of(a, len_of(a, lens, r));
+        const int32_t* row = table + (int64_t)r * a.max_pages;
+        for (int j = threadIdx.x; j < n; j += blockDim.x)
+            if (good_page(a, row[j])) atomicSub(refs + row[j], 1);
+    }
+    if (r < a.out_batch) {
+        const int len = parent >= 0 ? len_of(a, lens, parent) : 0;
+        const int n = pages_of(a, len);
+        const int32_t* row = table + (int64_t)max(parent, 0) * a.max_pages;
+        int32_t* out = out_table + (int64_t)r * a.max_pages;
+        for (int j = threadIdx.x; j < a.max_pages; j += blockDim.x) {
+            const int p = j < n ? row[j] : -1;
+            out[j] = p;
+            if (j < n && parent != r && good_page(a, p)) atomicAdd(refs + p, 1);
+        }
+        if (threadIdx.x == 0) out_lens[r] = len;
+    }
+}
+
+// ---------------------------------------------------------------- resize
+// One CTA. (1) every row's need of pages and the prefix sums over the rows; (2) a
+// scan of page_refs ranks the free pages, and the page of rank r goes to the row
+// whose range of ranks holds r; it ends once every need is met; (3) lengths,
+// releases and the counts of replaced pages (after the scan, so that nothing
+// freed here is taken here).
+__global__ void __launch_bounds__(kPlanThreads) resize_kernel(int32_t* table, int32_t* lens,
+                                                              const int32_t* new_lens,
+                                                              int32_t* refs, int32_t* src,
+                                                              int32_t* dst, PagesArgs a) {
+    extern __shared__ int pre[];  // [batch + 1]: ranks before each row
+    __shared__ int tmp[33];
+    ptx::griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int most = a.max_pages << a.ps_shift;
+    int total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int need = 0;
+        if (b < a.batch) {
+            const int old = len_of(a, lens, b), now = clamp_len(a.status, new_lens[b], most);
+            const int had = pages_of(a, old);
+            int shared = -1;
+            if (now > old) {
+                need = pages_of(a, now) - had;
+                if (old & (a.page_size - 1)) {
+                    const int p = table[(int64_t)b * a.max_pages + had - 1];
+                    if (good_page(a, p) && refs[p] > 1) {
+                        shared = p;
+                        ++need;
+                    }
+                }
+            }
+            src[b] = shared;
+            dst[b] = -1;
+        }
+        int sum;
+        const int before = block_scan(need, tmp, sum);
+        if (b < a.batch) pre[b] = total + before;
+        total += sum;
+    }
+    if (tid == 0) pre[a.batch] = total;
+    __syncthreads();
+
+    int found = 0;
+    for (int p0 = 0; p0 < a.num_pages && found < total; p0 += kRound) {
+        int r[kPer], free = 0, sum;
+        load_refs(refs, p0 + tid * kPer, a.num_pages, r);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) free += r[i] == 0;
+        int rank = found + block_scan(free, tmp, sum);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (r[i] != 0) continue;
+            if (rank < total) {
+                const int page = p0 + tid * kPer + i;
+                int lo = 0, hi = a.batch - 1;  // the last row that begins at or before rank
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (pre[mid] <= rank) lo = mid; else hi = mid - 1;
+                }
+                const bool swaps = src[lo] >= 0;
+                const int at = pages_of(a, len_of(a, lens, lo)) + rank - pre[lo] - (swaps ? 1 : 0);
+                table[(int64_t)lo * a.max_pages + at] = page;
+                if (swaps && rank == pre[lo]) dst[lo] = page;
+                refs[page] = 1;
+            }
+            ++rank;
+        }
+        found += sum;
+    }
+    __syncthreads();
+    if (found < total) {
+        if (tid == 0) report(a.status, MQA_STATUS_NO_PAGES);
+        for (int b = tid; b < a.batch; b += kPlanThreads) {
+            if (pre[b + 1] == pre[b] || pre[b + 1] <= found) continue;
+            // at most one row was given a part of its pages: they go back
+            const int had = pages_of(a, len_of(a, lens, b)) - (src[b] >= 0 ? 1 : 0);
+            int32_t* row = table + (int64_t)b * a.max_pages;
+            for (int r = pre[b]; r < found; ++r) {
+                const int at = had + r - pre[b];
+                refs[row[at]] = 0;
+                row[at] = r == pre[b] && src[b] >= 0 ? src[b] : -1;
+            }
+            src[b] = -1;
+            dst[b] = -1;
+        }
+        __syncthreads();
+    }
+
+    for (int b0 = (tid >> 5) * 32; b0 < a.batch; b0 += kPlanThreads) {
+        const int b = b0 + lane;
+        int had = 0, has = 0;
+        if (b < a.batch) {
+            const int old = len_of(a, lens, b);
+            int now = clamp_len(a.status, new_lens[b], most);
+            if (pre[b + 1] > found && pre[b + 1] > pre[b]) now = old;
+            had = pages_of(a, old);
+            has = pages_of(a, now);
+            if (src[b] >= 0) atomicSub(refs + src[b], 1);
+            lens[b] = now;
+        }
+        uint32_t shrinks = __ballot_sync(0xffffffffu, has < had);
+        while (shrinks) {
+            const int k = __ffs(shrinks) - 1;
+            shrinks &= shrinks - 1;
+            const int from = __shfl_sync(0xffffffffu, has, k), to = __shfl_sync(0xffffffffu, had, k);
+            int32_t* row = table + (int64_t)(b0 + k) * a.max_pages;
+            for (int j = from + lane; j < to; j += 32) {
+                if (good_page(a, row[j])) atomicSub(refs + row[j], 1);
+                row[j] = -1;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- compact
+// One CTA: counts the pages in use (N), ranks the used pages at N and above and
+// the free ones below N, pairs them, and moves the counts.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int32_t* refs, int32_t* src,
+                                                                    int32_t* dst, int32_t* count,
+                                                                    int32_t* map, PagesArgs a) {
+    __shared__ int tmp[33];
+    ptx::griddep_wait();
+    const int tid = threadIdx.x, half = a.num_pages / 2;
+    int live = 0;
+    for (int p = tid; p < a.num_pages; p += kPlanThreads) live += refs[p] > 0;
+    int n;
+    block_scan(live, tmp, n);
+    int moves = 0, holes = 0;
+    for (int p0 = 0; p0 < a.num_pages; p0 += kRound) {
+        int r[kPer], m = 0, h = 0, sum;
+        const int first = p0 + tid * kPer;
+        load_refs(refs, first, a.num_pages, r);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int p = first + i;
+            m += p < a.num_pages && p >= n && r[i] > 0;
+            h += p < n && r[i] <= 0;
+        }
+        // both counts stay below 2^16 a round: one scan for the two
+        const int both = block_scan(m | h << 16, tmp, sum);
+        int mr = moves + (both & 0xffff), hr = holes + (both >> 16);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int p = first + i;
+            if (p >= a.num_pages) break;
+            if (p >= n && r[i] > 0) src[mr++] = p;
+            if (p < n && r[i] <= 0) dst[hr++] = p;
+            map[p] = r[i] > 0 ? p : -1;
+        }
+        moves += sum & 0xffff;
+        holes += sum >> 16;
+    }
+    __syncthreads();
+    for (int i = tid; i < half; i += kPlanThreads) {
+        if (i < moves) {
+            const int s = src[i], d = dst[i];
+            map[s] = d;
+            refs[d] = refs[s];
+            refs[s] = 0;
+        } else {
+            src[i] = -1;
+            dst[i] = -1;
+        }
+    }
+    if (tid == 0) *count = moves;
+}
+
+__global__ void __launch_bounds__(128) compact_table_kernel(int32_t* table, const int32_t* lens,
+                                                            const int32_t* map, PagesArgs a) {
+    ptx::griddep_wait();
+    const int b = blockIdx.x;
+    const int n = pages_of(a, len_of(a, lens, b));
+    int32_t* row = table + (int64_t)b * a.max_pages;
+    for (int j = threadIdx.x; j < n; j += blockDim.x)
+        if (good_page(a, row[j])) row[j] = map[row[j]];
+}
+
+// ---------------------------------------------------------------- copy
+constexpr int kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
+    ptx::griddep_wait();
+    const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
+    const uint32_t chunks = a.chunks[blockIdx.y];
+    uint4* pool = static_cast<uint4*>(a.cache[blockIdx.y]);
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const int s = a.src[i], d = a.dst[i];
+        if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) {
+            if ((s != -1 || d != -1) && threadIdx.x == 0)
+                report_checked(a.status, MQA_STATUS_BAD_PAGE);
+            continue;
+        }
+        const uint4* from = pool + (int64_t)s * chunks;
+        uint4* to = pool + (int64_t)d * chunks;
+        uint32_t c = threadIdx.x;
+        for (; c + 3 * kCopyThreads < chunks; c += 4 * kCopyThreads) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = from[c + k * kCopyThreads];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[c + k * kCopyThreads] = v[k];
+        }
+        for (; c < chunks; c += kCopyThreads) to[c] = from[c];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const int32_t* table, const int32_t* lens, const int32_t* parents,
+                        int32_t* refs, int32_t* out_table, int32_t* out_lens, const PagesArgs& a,
+                        void* stream, bool pdl) {
+    return launch_pdl(fork_kernel, dim3(max(a.batch, a.out_batch)), dim3(128), 0, stream, pdl,
+                      table, lens, parents, refs, out_table, out_lens, a);
+}
+
+cudaError_t launch_resize(int device, int32_t* table, int32_t* lens, const int32_t* new_lens,
+                          int32_t* refs, int32_t* src, int32_t* dst, const PagesArgs& a,
+                          void* stream, bool pdl) {
+    static uint32_t done[64];
+    const uint32_t smem = (uint32_t)(a.batch + 1) * 4;
+    if (smem > 40000) {
+        const cudaError_t e = allow_smem(resize_kernel, device, smem, done);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(resize_kernel, dim3(1), dim3(kPlanThreads), smem, stream, pdl, table, lens,
+                      new_lens, refs, src, dst, a);
+}
+
+cudaError_t launch_compact(int32_t* table, const int32_t* lens, int32_t* refs, int32_t* src,
+                           int32_t* dst, int32_t* count, int32_t* map, const PagesArgs& a,
+                           void* stream, bool pdl) {
+    cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pdl,
+                               refs, src, dst, count, map, a);
+    if (e != cudaSuccess || a.batch == 0) return e;
+    return launch_pdl(compact_table_kernel, dim3(a.batch), dim3(128), 0, stream, pdl, table, lens,
+                      map, a);
+}
+
+cudaError_t launch_copy(const CopyArgs& a, void* stream, bool pdl) {
+    const int x = a.n < 4096 ? a.n : 4096;
+    return launch_pdl(copy_kernel, dim3(x, a.num_caches), dim3(kCopyThreads), 0, stream, pdl, a);
+}
+
+}  // namespace mqa

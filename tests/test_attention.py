@@ -1,0 +1,420 @@
+"""Attention over the FP4 cache against a row-by-row reference in 64 bits, at the
+lengths, masks, head layouts and lists where it can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+import paged_mqa_logits_b200 as mq
+from tests import cache_ref as ref
+
+gpu = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+class Case:
+    """Inputs on the CPU: pages of a shuffled pool with spare pages; every slot that
+    no row can see, and every spare page, holds NaN scales and full codes."""
+
+    def __init__(self, ctx, nn, H, Hk, D, ps, dtype="bf16", seed=0, k=None, q_gain=2.0, spare=3,
+                 width=None):
+        g = torch.Generator().manual_seed(seed)
+        self.ctx = torch.tensor(ctx, dtype=torch.int32)
+        B = len(ctx)
+        counts = [-(-max(c, 0) // ps) for c in ctx]
+        width = width or max(max(counts), 1) + 1
+        P = sum(counts) + spare
+        order = torch.randperm(P, generator=g).to(torch.int32)
+        self.table = torch.full((B, width), -1, dtype=torch.int32)
+        at = 0
+        for b, n in enumerate(counts):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.nn, self.H, self.Hk, self.D, self.ps, self.dtype = nn, H, Hk, D, ps, TYPES[dtype]
+        self.q = (q_gain * torch.randn(B, nn, H, D, generator=g)).to(self.dtype)
+        self.k = self.pool(P, g)
+        self.v = self.pool(P, g)
+        seen = torch.zeros(P, ps, dtype=torch.bool)
+        for b, c in enumerate(ctx):
+            for t in range(max(c, 0)):
+                seen[self.table[b, t // ps].long(), t % ps] = True
+        for pool in (self.k, self.v):
+            codes, scales = self.split(pool)
+            codes[~seen[:, None].expand(-1, Hk, -1)] = 0xF7
+            scales[~seen[:, None].expand(-1, Hk, -1)] = 0x7F
+        self.indices = None
+        if k:
+            self.indices = torch.full((B, nn, k), -1, dtype=torch.int32)
+            for b in range(B):
+                for n in range(nn):
+                    upto = min(max(ctx[b] - nn + 1 + n, 0), max(ctx[b], 0))
+                    pick = torch.randperm(upto, generator=g)[:k] if upto else torch.zeros(0)
+                    self.indices[b, n, :len(pick)] = pick.sort().values.to(torch.int32)
+        self.scale = D ** -0.5
+
+    def pool(self, P, g):
+        x = torch.randn(P, self.Hk, self.ps, self.D, generator=g, dtype=torch.float64)
+        x *= torch.exp(torch.randn(P, self.Hk, self.ps, 1, generator=g, dtype=torch.float64))
+        codes, scales, _ = ref.quantise_fp4(x.numpy())
+        both = np.concatenate((codes.reshape(P, self.Hk, -1), scales.reshape(P, self.Hk, -1)), -1)
+        return torch.from_numpy(both.reshape(P, -1).copy())
+
+    def split(self, pool):
+        c = pool.view(pool.shape[0], self.Hk, -1)
+        n = self.ps * self.D // 2
+        return c[..., :n].unflatten(-1, (self.ps, self.D // 2)), c[..., n:].unflatten(-1, (self.ps, self.D // 16))
+
+    def gpu(self):
+        return {n: getattr(self, n).cuda() for n in ("q", "k", "v", "table", "ctx")} | \
+            {"indices": None if self.indices is None else self.indices.cuda()}
+
+    def call(self, d, num_ctas=None, **kw):
+        sched = None if self.indices is not None else mq.mqa_logits_schedule(d["ctx"], num_ctas)
+        return mq.paged_mqa_attention_fp4(d["q"], d["k"], d["v"], d["table"], d["ctx"], sched,
+                                          kv_heads=self.Hk, scale=self.scale, indices=d["indices"],
+                                          page_size=self.ps, **kw)
+
+    def reference(self):
+        return ref.attention(self.q, self.k, self.v, self.table, self.ctx, heads_kv=self.Hk,
+                             ps=self.ps, scale=self.scale, indices=self.indices)
+
+    def check(self, got, lse=None):
+        T = max([1, *self.ctx.tolist()]) if self.indices is None else self.indices.shape[2]
+        ref.check_attention(got, lse, self.reference(), T, self.dtype)
+
+    def run_and_check(self, num_ctas=None):
+        mq.mqa_logits_clear_status()
+        out, lse = self.call(self.gpu(), num_ctas, with_lse=True)
+        torch.cuda.synchronize()
+        self.check(out, lse)
+        assert mq.mqa_logits_get_status() == 0
+
+
+DENSE = [
+    # ctx, next_n, H, Hk, D, page size, type, CTAs
+    ([1], 1, 1, 1, 64, 16, "bf16", None),
+    ([0, 1, 2, 0, 3], 4, 2, 1, 128, 16, "f16", None),
+    ([31, 32, 33, 63, 64, 65], 1, 8, 1, 128, 32, "bf16", None),
+    ([255, 256, 257, 0, 511, 513], 2, 16, 2, 128, 64, "bf16", None),
+    ([700, 5, 300], 3, 15, 3, 64, 16, "f16", 5),
+    ([1000, 0, 129], 1, 32, 1, 128, 256, "f16", 2),
+    ([640, 130, 1], 2, 64, 1, 128, 64, "bf16", 3),
+    ([900], 1, 128, 1, 64, 128, "bf16", None),
+    ([333, 90], 1, 34, 2, 64, 64, "bf16", 1),
+    ([450, 17], 4, 24, 1, 128, 16, "bf16", None),
+    ([777, 256], 1, 100, 1, 128, 64, "f16", 7),
+    ([2500, 0, 0, 1200], 1, 7, 1, 128, 64, "bf16", 4),
+    ([1600], 2, 8, 8, 64, 32, "f16", None),
+    ([400] * 9, 1, 5, 5, 128, 16, "bf16", 148),
+    ([600, 257], 1, 48, 1, 128, 16, "bf16", 3),
+    ([1100, 3], 2, 33, 1, 64, 32, "f16", 4),
+    ([520, 100, 256], 1, 65, 1, 64, 256, "bf16", 2),
+    ([3000, 1], 4, 32, 1, 128, 64, "bf16", 6),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", DENSE, ids=[f"{c[0][0]}-n{c[1]}-h{c[2]}.{c[3]}-d{c[4]}-p{c[5]}" for c in DENSE])
+def test_every_cached_token(case):
+    *shape, dtype, ctas = case
+    Case(*shape, dtype, seed=10 + DENSE.index(case)).run_and_check(ctas)
+
+
+LISTS = [
+    ([500, 0, 3, 70], 1, 8, 1, 128, 64, "bf16", 64),
+    ([500, 1, 40], 3, 21, 3, 64, 16, "f16", 77),
+    ([2000, 300], 2, 32, 1, 128, 64, "bf16", 1000),
+    ([1500], 1, 128, 1, 128, 64, "f16", 513),
+    ([64, 900], 4, 17, 1, 64, 32, "bf16", 31),
+    ([40], 1, 1, 1, 64, 16, "bf16", 1),
+    ([1200, 5], 1, 64, 1, 128, 64, "bf16", 300),
+    ([800, 5], 1, 96, 2, 64, 256, "bf16", 200),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", LISTS, ids=[f"{c[0][0]}-n{c[1]}-h{c[2]}.{c[3]}-d{c[4]}-k{c[7]}" for c in LISTS])
+def test_listed_tokens(case):
+    *shape, dtype, k = case
+    Case(*shape, dtype, seed=40 + LISTS.index(case), k=k).run_and_check()
+
+
+@gpu
+def test_lists_with_holes_repeats_and_tokens_out_of_sight():
+    """-1 anywhere, tokens at and past the context, negatives, a token twice, and a
+    position whose list is empty."""
+    c = Case([300, 200, 90], 2, 8, 1, 128, 16, seed=60, k=100)
+    g = torch.Generator().manual_seed(1)
+    holes = torch.rand(c.indices.shape, generator=g) < 0.3
+    c.indices[holes] = -1
+    c.indices[0, 0, 3] = 299      # position 0 of two does not see the row's last token
+    c.indices[0, 1, 3] = 300
+    c.indices[0, 1, 4] = 2 ** 31 - 1
+    c.indices[1, 0, 5:9] = -2 ** 31
+    c.indices[1, 1, 10:14] = 17   # counted four times
+    c.indices[2, 0] = -1
+    c.run_and_check()
+    c.indices[:, :, :] = -1
+    d = c.gpu()
+    out, lse = c.call(d, with_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@gpu
+def test_scores_that_rise_along_the_row():
+    """Every tile raises the running reference; large and tiny rows of q."""
+    for rising in (1, -1):
+        c = Case([1500, 700], 1, 20, 1, 128, 64, seed=61, q_gain=1.0)
+        codes, scales = c.split(c.k)
+        for b in range(2):
+            t = torch.arange(int(c.ctx[b]))
+            size = 60 + (t * 58 // int(c.ctx[b]) if rising > 0 else 58 - t * 58 // int(c.ctx[b]))
+            scales[c.table[b][t // 64].long(), 0, t % 64] = size[:, None].to(torch.uint8)
+        c.run_and_check()
+    c = Case([300, 200, 100], 1, 4, 1, 128, 64, seed=62)
+    q = c.q.float()
+    q[0] *= 1e-20
+    q[1] *= 2e4
+    q[1, 0, 2] = 0
+    c.q = q.to(torch.bfloat16)
+    c.scale = 1e-5
+    c.run_and_check()
+
+
+@gpu
+@pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
+def test_scales(scale):
+    c = Case([290, 31], 2, 6, 2, 64, 32, "f16", seed=63, q_gain=0.5)
+    c.scale = scale
+    c.run_and_check()
+
+
+@gpu
+def test_strided_q_own_buffers_and_a_poisoned_workspace():
+    c = Case([700, 0, 290], 2, 12, 2, 128, 64, seed=64)
+    d = c.gpu()
+    want, lse = c.call(d, with_lse=True)
+    wide = torch.randn(3, 2, 3, 16, 128, device="cuda").to(torch.bfloat16)  # a fused projection's output
+    view = wide[:, :, 1, 2:14]
+    view.copy_(d["q"])
+    assert not view.is_contiguous()
+    work = mq.mqa_attention_workspace(view, kv_heads=2)
+    work.view(torch.float32).fill_(float("nan"))
+    out = torch.full_like(d["q"], float("nan"))
+    d["q"] = view
+    got, l2 = c.call(d, out=out, lse=torch.full_like(lse, float("nan")), workspace=work)
+    assert got.data_ptr() == out.data_ptr()
+    assert torch.equal(got, want) and torch.equal(l2, lse)
+    c.check(got, l2)
+    # one buffer for K and V
+    c.v, d["v"] = c.k, d["k"]
+    c.check(*c.call(d, with_lse=True))
+
+
+@gpu
+def test_bad_pages_are_clamped_and_reported():
+    c = Case([300, 100], 1, 4, 1, 64, 16, seed=65, spare=0)
+    c.table[0, 2] = c.k.shape[0] + 5
+    c.table[1, 0] = -9
+    d = c.gpu()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for kw in ({}, {"flags": mq.MQA_FLAG_VALIDATE, "status": status}):
+        out, lse = c.call(d, with_lse=True, **kw)
+        c.check(out, lse)
+    assert int(status) == mq.MQA_STATUS_BAD_PAGE
+    mq.mqa_logits_clear_status()
+
+
+@gpu
+def test_lengths_beyond_the_table_and_negative_ones():
+    c = Case([128, 64, 32], 1, 4, 1, 64, 16, seed=66, width=8)
+    d = c.gpu()
+    c.ctx[0], c.ctx[1] = 5000, -3   # the first row's table holds 128 tokens
+    d["ctx"] = c.ctx.cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sched = mq.mqa_logits_schedule(d["ctx"])
+    out, lse = mq.paged_mqa_attention_fp4(d["q"], d["k"], d["v"], d["table"], d["ctx"], sched,
+                                          scale=c.scale, page_size=16, with_lse=True,
+                                          flags=mq.MQA_FLAG_VALIDATE, status=status)
+    assert int(status) & mq.MQA_STATUS_BAD_CONTEXT
+    c.check(out, lse)
+    mq.mqa_logits_clear_status()
+
+
+@gpu
+def test_stale_schedule_is_reported():
+    c = Case([600, 300], 1, 4, 1, 64, 16, seed=67)
+    d = c.gpu()
+    sched = mq.mqa_logits_schedule(torch.tensor([600, 10], dtype=torch.int32, device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mq.paged_mqa_attention_fp4(d["q"], d["k"], d["v"], d["table"], d["ctx"], sched, page_size=16,
+                               flags=mq.MQA_FLAG_VALIDATE, status=status)
+    assert int(status) & mq.MQA_STATUS_STALE_SCHEDULE
+    mq.mqa_logits_clear_status()
+
+
+@gpu
+@pytest.mark.parametrize("k", [None, 600], ids=["all", "list"])
+def test_captured_replayed_and_on_another_stream(k):
+    """A replay follows new lengths, queries and cache contents; two graphs with a
+    workspace each, and a call on a stream of its own, give the eager results."""
+    a, b = (Case(x, 2, 16, 1, 128, 64, seed=70 + i, k=k, width=20)
+            for i, x in enumerate(([900, 0, 300], [100, 1200, 513])))
+    P = max(a.k.shape[0], b.k.shape[0])
+    grow = lambda t: torch.cat((t, torch.full((P - t.shape[0], t.shape[1]), 0x7F, dtype=torch.uint8)))  # noqa: E731
+    for c in (a, b):
+        c.k, c.v = grow(c.k), grow(c.v)
+    da, db = a.gpu(), b.gpu()
+    want = [c.call(d, with_lse=True) for c, d in ((a, da), (b, db))]
+    a.check(*want[0])
+    b.check(*want[1])
+    live = [{n: None if t is None else t.clone() for n, t in da.items()} for _ in range(2)]
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    for d in live:
+        work = mq.mqa_attention_workspace(d["q"], topk=k or 0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(a.call(d, with_lse=True, workspace=work))
+        graphs.append(g)
+    for src, w in ((da, want[0]), (db, want[1]), (da, want[0])):
+        for d in live:
+            for n, t in d.items():
+                if t is not None:
+                    t.copy_(src[n])
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sched = None if k else mq.mqa_logits_schedule(db["ctx"])
+    s.wait_stream(torch.cuda.current_stream())
+    got = mq.paged_mqa_attention_fp4(db["q"], db["k"], db["v"], db["table"], db["ctx"], sched,
+                                     scale=b.scale, indices=db["indices"], page_size=64, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want[1][0])
+
+
+@gpu
+def test_pages_behind_four_gigabytes():
+    """Byte offsets past 2^32 in a pool of 9 million pages."""
+    c = Case([200, 90], 1, 8, 1, 64, 16, seed=80)
+    P = 9_000_000
+    assert P * c.k.shape[1] > 2 ** 32
+    big = torch.empty(P, c.k.shape[1], dtype=torch.uint8, device="cuda")
+    d = c.gpu()
+    n = c.k.shape[0]
+    big[P - n:] = d["k"]
+    d["k"] = d["v"] = big
+    c.v = c.k
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (P - n), -1).to(torch.int32)
+    out, lse = c.call(d, with_lse=True)
+    c.check(out, lse)
+
+
+@gpu
+def test_position_of_the_split_changes_nothing_but_rounding():
+    """Every number of CTAs covers every token once; the same call twice is the same."""
+    c = Case([3000, 17, 1024], 2, 8, 1, 128, 64, seed=81)
+    d = c.gpu()
+    for ctas in (1, 2, 3, 13, 148, 300):
+        out, lse = c.call(d, ctas, with_lse=True)
+        again, l2 = c.call(d, ctas, with_lse=True)
+        assert torch.equal(out, again) and torch.equal(lse, l2)
+        c.check(out, lse)
+
+
+# ---------------------------------------------------------------- refusals (CPU)
+def params(**kw):
+    base = dict(batch=2, next_n=1, num_heads=8, num_kv_heads=2, head_dim=128, page_size=64,
+                num_pages=4, max_pages_per_row=2, topk=0, num_ctas=148, dtype=0, flags=0,
+                softmax_scale=1.0, reserved=0, q_stride_b=1024, q_stride_n=1024, q_stride_h=128,
+                workspace_bytes=1 << 40, status=None)
+    base.update(kw)
+    return mq.AttentionParams(**base)
+
+
+@pytest.mark.parametrize("kw,code,needle", [
+    (dict(batch=-1), -1, "batch"), (dict(batch=40000), -1, "batch"), (dict(next_n=0), -1, "next_n"), (dict(next_n=5), -1, "next_n"),
+    (dict(num_heads=7), -1, "num_kv_heads"), (dict(num_kv_heads=0), -1, "num_kv_heads"),
+    (dict(num_heads=260), -4, "128"), (dict(num_heads=128, next_n=4, num_kv_heads=2), -4, "128"),
+    (dict(head_dim=96), -4, "head_dim"), (dict(head_dim=32), -4, "head_dim"),
+    (dict(page_size=8), -1, "page_size"), (dict(page_size=48), -1, "page_size"),
+    (dict(page_size=512), -1, "page_size"), (dict(num_pages=0), -1, "num_pages"),
+    (dict(num_pages=2 ** 30), -4, "2^31"), (dict(max_pages_per_row=0), -1, "max_pages"),
+    (dict(topk=-1), -1, "topk"), (dict(num_ctas=0), -1, "num_ctas"),
+    (dict(num_ctas=5000), -1, "num_ctas"), (dict(dtype=2), -1, "dtype"), (dict(flags=4), -1, "flag"),
+    (dict(q_stride_h=132), -1, "strides"), (dict(status=2), -1, "aligned"),
+])
+def test_bad_params(kw, code, needle):
+    import ctypes
+    lib, p = mq.library(), params(**kw)
+    assert lib.paged_mqa_attention_fp4(16, 16, 16, 16, 16, 16, None, 16, None, 16, ctypes.byref(p), None) == code
+    assert needle in lib.mqa_logits_last_error().decode()
+
+
+def test_bad_pointers():
+    import ctypes
+    lib, p = mq.library(), params()
+    good = [16, 16, 16, 16, 16, 16, None, 16, None, 16]
+    for i in (0, 1, 2, 3, 4, 5, 7):
+        args = list(good)
+        args[i] = None
+        assert lib.paged_mqa_attention_fp4(*args, ctypes.byref(p), None) == -1
+        assert "NULL" in lib.mqa_logits_last_error().decode()
+    for i, bad in ((0, 24), (1, 8), (2, 8), (3, 18), (4, 18), (5, 18), (7, 8), (8, 18), (9, 24)):
+        args = list(good)
+        args[i] = bad
+        assert lib.paged_mqa_attention_fp4(*args, ctypes.byref(p), None) == -1
+        assert "aligned" in lib.mqa_logits_last_error().decode()
+    assert lib.paged_mqa_attention_fp4(*good, None, None) == -1
+    lists = params(topk=8)
+    assert lib.paged_mqa_attention_fp4(*good, ctypes.byref(lists), None) == -1
+    assert "indices" in lib.mqa_logits_last_error().decode()
+    assert lib.paged_mqa_attention_fp4(*[None] * 10, ctypes.byref(params(batch=0)), None) == 0
+    size = ctypes.c_uint64(7)
+    assert lib.mqa_attention_workspace_size(ctypes.byref(params(batch=0)), ctypes.byref(size)) == 0
+    assert size.value == 0
+    assert lib.mqa_attention_workspace_size(ctypes.byref(p), None) == -1
+
+
+def test_params_struct_layout_matches_header():
+    import ctypes
+    assert ctypes.sizeof(mq.AttentionParams) == 96
+    assert mq.AttentionParams.softmax_scale.offset == 48 and mq.AttentionParams.q_stride_b.offset == 56
+    assert mq.AttentionParams.workspace_bytes.offset == 80 and mq.AttentionParams.status.offset == 88
+
+
+def test_binding_checks_shapes():
+    q = torch.zeros(2, 1, 8, 128, dtype=torch.bfloat16)
+    kv = torch.zeros(4, 2 * 64 * 72, dtype=torch.uint8)
+    bt, ctx = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    idx, sched = torch.zeros(2, 1, 4, dtype=torch.int32), torch.zeros(149, 2, dtype=torch.int32)
+
+    def call(q=q, k=kv, v=kv, bt=bt, ctx=ctx, sched=sched, **kw):
+        return mq.paged_mqa_attention_fp4(q, k, v, bt, ctx, sched, kv_heads=2, **kw)
+
+    with pytest.raises(ValueError, match="q must be"):
+        call(q=q[0])
+    with pytest.raises(ValueError, match="either"):
+        call(indices=idx)
+    with pytest.raises(ValueError, match="either"):
+        call(sched=None)
+    with pytest.raises(ValueError, match="dtype"):
+        call(q=q.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q=q.transpose(2, 3).contiguous().transpose(2, 3))
+    with pytest.raises(ValueError, match="differ"):
+        call(v=kv[:3])
+    with pytest.raises(ValueError, match="pages hold"):
+        call(page_size=32)
+    with pytest.raises(ValueError, match="indices must"):
+        call(sched=None, indices=idx[:1])
+    with pytest.raises(ValueError, match="at least one"):
+        call(sched=None, indices=idx[:, :, :0])
+    with pytest.raises(ValueError, match="CUDA"):
+        call()  # host tensors: no CPU path
