@@ -6,11 +6,13 @@
 // exceeds it by kSlack, so p <= 2^kSlack fits f16 and most tiles need no rescale.
 //
 // One warp takes 32 tokens at a time through its own ring of asynchronous copies
-// (no CTA barrier inside a row), dequantises K and V straight into the fragments
-// of mma.sync.m16n8k16 (f16 x f16 -> f32; code * scale has at most 6 significant
-// bits and is exact in f16), and keeps O for 16 * MT query rows in registers. At
-// the end of a row the CTA's warps join their (m, sum, O) through shared memory;
-// rows that several CTAs share leave partial results, which combine_kernel joins.
+// (no CTA barrier inside a row) and dequantises K and V straight into the A
+// fragments of mma.sync.m16n8k16 (f16 x f16 -> f32; code * scale has at most 6
+// significant bits and is exact in f16): S^T = K Q^T (16 tokens x 8 query rows),
+// then O^T += V^T P^T, whose B operand is S^T's result transposed within the warp.
+// The query rows are N, so 8 rows cost 8 and not 16. At the end of a row the CTA's
+// warps join their (m, sum, O) through shared memory; rows that several CTAs share
+// leave partial results, which combine_kernel joins.
 #include "common.cuh"
 
 #include "attention.cuh"
@@ -19,22 +21,26 @@
 namespace mqa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kSpan = 32;         // tokens of a ring slot
 constexpr float kUnset = -1e30f;  // m of a row that has seen no token
 constexpr float kSlack = 8.f;     // p <= 2^8
 
-template <int D>
+// NT: query rows of a CTA / 8. More rows take more registers, so fewer warps.
+template <int D, int NT>
 struct Shape {
+    static constexpr int kWarps = NT == 1 ? 16 : NT == 2 ? 12 : 8;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kRow = D / 2;                       // code bytes of a token
     static constexpr int kScales = D / 16;                   // scale bytes of a token
     static constexpr int kSlot = 2 * kSpan * (kRow + kScales);  // K codes, V codes, K scales, V scales
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = 2 * 128 / D;
     static constexpr int kRing = kWarps * kStages * kSlot;
-    static constexpr int kLane = D / 4 + 4;                  // floats of a lane's share of a row of O, padded
-    static constexpr int kRed = kWarps * 16 * 4 * kLane * 4; // bytes: every warp's 16 rows of O
-    static constexpr int kSmem = kRing + kRed + kWarps * 16 * 4 * 4;
+    static constexpr int kLane = D / 8;                      // floats that a lane leaves of a row of O
+    static constexpr int kRedRow = D + 4;                    // floats of a row, padded
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRed = kWarps * kRows * kRedRow * 4;
+    static constexpr int kSmem = kRing + kRed + kWarps * kRows * 4 * 4;
+    static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -51,6 +57,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of f16 that the warp holds as fragments.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // Eight e2m1 codes as four f16 pairs; byte i becomes pair i (low nibble first).
@@ -178,45 +191,32 @@ __device__ __forceinline__ bool settle(const AttentionArgs& a, Walk& w, int u0) 
     return false;
 }
 
-template <int D, int MT, typename T, bool kList>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttentionArgs a) {
-    using S = Shape<D>;
-    constexpr int kSteps = D / 16;   // contraction steps of Q K^T
-    constexpr int kTiles = D / 8;    // column tiles of O
-    constexpr int kElems = D / 4;    // elements of a row that one lane of a quad holds
+// The parts of the schedule that CTA i of a dense launch takes: with Hk kv heads the
+// Hk * S (head, part) pairs are dealt in order, Hk to each CTA, so that a CTA walks
+// up to Hk neighbouring parts of one head as one range and rows are cut S + Hk
+// times over all heads. Range k of head hk begins at part range_start(hk, k).
+__host__ __device__ inline int range_start(int hk, int k, int heads, int S) {
+    const int first = (int)(((int64_t)hk * S) % heads);  // parts of the head in its first CTA: heads - first
+    return k == 0 ? 0 : min(S, k * heads - first);
+}
+
+template <int D, int NT, typename T, bool kList>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(const AttentionArgs a) {
+    using S = Shape<D, NT>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
+    constexpr int kTiles = D / 16;   // row tiles of O^T, and contraction steps of K Q^T
+    constexpr int kElems = D / 4;    // elements of a row of q or K that one lane of a quad holds
     extern __shared__ __align__(128) uint8_t smem[];
     float* red = reinterpret_cast<float*>(smem + S::kRing);
-    float* red_ml = reinterpret_cast<float*>(smem + S::kRing + S::kRed);  // [warp][16][4]
+    float* red_ml = reinterpret_cast<float*>(smem + S::kRing + S::kRed);  // [warp][row][4]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const uint32_t ring = ptx::smem_u32(smem) + warp * (S::kStages * S::kSlot);
-    const int hk = blockIdx.y % a.kv_heads;
-    const int row0 = (blockIdx.y / a.kv_heads) * (16 * MT);  // first query row of this CTA
+    const int row0 = blockIdx.y * S::kRows;  // first query row of this CTA
 
     ptx::griddep_wait();
 
-    // ---- this CTA's range
-    Walk w;
-    int draft = 0;
-    bool more;
-    if constexpr (kList) {
-        w.item = blockIdx.x / a.splits;
-        const int sp = blockIdx.x - w.item * a.splits;
-        w.b = w.item / a.next_n;
-        draft = w.item - w.b * a.next_n;
-        const int full = row_ctx<kList>(a, w.b);
-        w.ctx = min(max(full - a.next_n + 1 + draft, 0), full);
-        const int per = ((a.topk + a.splits - 1) / a.splits + kSpan - 1) / kSpan * kSpan;
-        w.t0 = min(a.topk, sp * per);
-        w.t1 = min(a.topk, w.t0 + per);
-        more = true;
-    } else {
-        const int i = blockIdx.x;
-        w.b = max(__ldg(a.schedule + 2 * i), 0);
-        const int u0 = max(__ldg(a.schedule + 2 * i + 1), 0);
-        w.last_b = __ldg(a.schedule + 2 * i + 2);
-        w.last_u = __ldg(a.schedule + 2 * i + 3);
-        more = settle(a, w, u0);
+    if constexpr (!kList) {
         if ((a.status.flags & MQA_FLAG_VALIDATE) && blockIdx.y == 0 && warp == 0) {
             KernelArgs ka{};
             ka.context_lens = a.context_lens;
@@ -225,121 +225,147 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttentionA
             ka.lib_status = a.status.lib;
             ka.batch = a.batch;
             ka.num_ctas = a.num_ctas;
-            check_schedule(ka, i, lane);
+            check_schedule(ka, blockIdx.x, lane);
         }
         // rows without tokens are in no CTA's range: their results are written here
-        for (int b = i; b < a.batch; b += a.num_ctas) {
+        for (int b = blockIdx.x; b < a.batch; b += a.num_ctas) {
             if (__ldg(a.context_lens + b) > 0) continue;
-            for (int j = threadIdx.x; j < a.next_n * a.group * (D / 8); j += kThreads) {
-                const int r = j / (D / 8), n = r / a.group, h = hk * a.group + r - n * a.group;
-                if (r < row0 || r >= row0 + 16 * MT) continue;
-                const int64_t o = ((int64_t)b * a.next_n + n) * a.heads + h;
-                reinterpret_cast<uint4*>(a.out)[o * (D / 8) + j % (D / 8)] = make_uint4(0, 0, 0, 0);
-                if (a.lse != nullptr && j % (D / 8) == 0) a.lse[o] = -INFINITY;
-            }
+            const int64_t o = (int64_t)b * a.next_n * a.heads;
+            for (int j = threadIdx.x; j < a.next_n * a.heads * (D / 8); j += kThreads)
+                reinterpret_cast<uint4*>(a.out)[o * (D / 8) + j] = make_uint4(0, 0, 0, 0);
+            if (a.lse != nullptr)
+                for (int j = threadIdx.x; j < a.next_n * a.heads; j += kThreads) a.lse[o + j] = -INFINITY;
         }
     }
 
-    // ---- loads: a walk that runs ahead of the computation by kStages - 1 chunks
-    Walk lw = w;
-    bool lmore = more;
-    int lpos = lw.t0 + warp * kSpan;  // next chunk to resolve
-    // The cache slot (page * page_size + slot) of this lane's token of the next
-    // chunk, -1 for none, found one step before its copies are issued.
-    int next_slot = -1;
-    bool next_any = false;             // the chunk exists
-    const int32_t* list = kList ? a.indices + (int64_t)w.item * a.topk : nullptr;
-
-    auto resolve = [&]() {
-        next_any = false;
-        next_slot = -1;
+    int pair = kList ? 0 : blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
+    const int pairs_end = pair + a.kv_heads;
+    do {
+        // ---- one range of rows of one kv head
+        Walk w;
+        int draft = 0, part = 0, hk;
+        bool more;
         if constexpr (kList) {
-            if (lpos >= lw.t1) return;
+            hk = blockIdx.x % a.kv_heads;
+            const int x = blockIdx.x / a.kv_heads;
+            w.item = x / a.splits;
+            part = x - w.item * a.splits;
+            w.b = w.item / a.next_n;
+            draft = w.item - w.b * a.next_n;
+            const int full = row_ctx<kList>(a, w.b);
+            w.ctx = min(max(full - a.next_n + 1 + draft, 0), full);
+            const int per = ((a.topk + a.splits - 1) / a.splits + kSpan - 1) / kSpan * kSpan;
+            w.t0 = min(a.topk, part * per);
+            w.t1 = min(a.topk, w.t0 + per);
+            more = true;
         } else {
-            while (lmore && lpos >= lw.t1) {
-                ++lw.b;
-                lmore = settle(a, lw, 0);
-                lpos = lw.t0 + warp * kSpan;
-            }
-            if (!lmore) return;
+            hk = pair / a.num_ctas;
+            part = pair - hk * a.num_ctas;
+            const int n = min(a.num_ctas - part, pairs_end - pair);
+            pair += n;
+            w.b = max(__ldg(a.schedule + 2 * part), 0);
+            const int u0 = max(__ldg(a.schedule + 2 * part + 1), 0);
+            w.last_b = __ldg(a.schedule + 2 * (part + n));
+            w.last_u = __ldg(a.schedule + 2 * (part + n) + 1);
+            more = settle(a, w, u0);
         }
-        next_any = true;
-        int t = lpos + lane;
-        lpos += kWarps * kSpan;
-        bool ok = t < lw.t1;
-        if constexpr (kList) {
-            t = ok ? __ldg(list + t) : -1;
-            ok = t >= 0 && t < lw.ctx;
-        }
-        if (ok) {
-            int page = __ldg(a.block_table + (int64_t)lw.b * a.max_pages + (t >> a.ps_shift));
-            if (page < 0 || page >= a.num_pages) {
-                report_checked(a.status, MQA_STATUS_BAD_PAGE);
-                page = page < 0 ? 0 : a.num_pages - 1;
-            }
-            next_slot = (page << a.ps_shift) | (t & (a.page_size - 1));
-        }
-    };
 
-    const int64_t head_at = (int64_t)hk * a.page_size * (S::kRow + S::kScales);
-    uint32_t seen = 0;  // selected: lane s keeps the mask of the visible tokens in ring slot s
-    auto issue = [&](int stage) {
-        if (next_any) {
-            const uint32_t base = ring + stage * S::kSlot;
-            constexpr int kPieces = S::kRow / 16;       // 16-byte pieces of a token's codes
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
-                const int at = __shfl_sync(0xffffffffu, next_slot, t);
-                const int64_t off = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
-                                    (int64_t)(max(at, 0) & (a.page_size - 1)) * S::kRow + o;
-                copy_async<16>(base + code_at<D>(t, o), a.k + off, at >= 0);
-                copy_async<16>(base + kSpan * S::kRow + code_at<D>(t, o), a.v + off, at >= 0);
-            }
-            const int at = max(next_slot, 0);
-            const int64_t off = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
-                                (int64_t)a.page_size * S::kRow +
-                                (int64_t)(at & (a.page_size - 1)) * S::kScales;
-            const uint32_t sc = base + 2 * kSpan * S::kRow + lane * S::kScales;
-            copy_async<S::kScales>(sc, a.k + off, next_slot >= 0);
-            copy_async<S::kScales>(sc + kSpan * S::kScales, a.v + off, next_slot >= 0);
+        // ---- loads: a walk that runs ahead of the computation by kStages - 1 spans
+        Walk lw = w;
+        bool lmore = more;
+        int lpos = lw.t0 + warp * kSpan;  // next span to resolve
+        // The cache slot (page * page_size + slot) of this lane's token of the next
+        // span, -1 for none, found one step before its copies are issued.
+        int next_slot = -1;
+        bool next_any = false;            // the span exists
+        const int32_t* list = kList ? a.indices + (int64_t)w.item * a.topk : nullptr;
+
+        auto resolve = [&]() {
+            next_any = false;
+            next_slot = -1;
             if constexpr (kList) {
-                const uint32_t m = __ballot_sync(0xffffffffu, next_slot >= 0);
-                if (lane == stage) seen = m;
+                if (lpos >= lw.t1) return;
+            } else {
+                while (lmore && lpos >= lw.t1) {
+                    ++lw.b;
+                    lmore = settle(a, lw, 0);
+                    lpos = lw.t0 + warp * kSpan;
+                }
+                if (!lmore) return;
             }
-        }
-        ptx::cp_async_commit();
+            next_any = true;
+            int t = lpos + lane;
+            lpos += kWarps * kSpan;
+            bool ok = t < lw.t1;
+            if constexpr (kList) {
+                t = ok ? __ldg(list + t) : -1;
+                ok = t >= 0 && t < lw.ctx;
+            }
+            if (ok) {
+                int page = __ldg(a.block_table + (int64_t)lw.b * a.max_pages + (t >> a.ps_shift));
+                if (page < 0 || page >= a.num_pages) {
+                    report_checked(a.status, MQA_STATUS_BAD_PAGE);
+                    page = page < 0 ? 0 : a.num_pages - 1;
+                }
+                next_slot = (page << a.ps_shift) | (t & (a.page_size - 1));
+            }
+        };
+
+        const int64_t head_at = (int64_t)hk * a.page_size * (S::kRow + S::kScales);
+        uint32_t seen = 0;  // selected: lane s keeps the mask of the visible tokens in ring slot s
+        auto issue = [&](int stage) {
+            if (next_any) {
+                const uint32_t base = ring + stage * S::kSlot;
+                constexpr int kPieces = S::kRow / 16;       // 16-byte pieces of a token's codes
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
+                    const int at = __shfl_sync(0xffffffffu, next_slot, t);
+                    const int64_t off = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
+                                        (max(at, 0) & (a.page_size - 1)) * S::kRow + o;
+                    copy_async<16>(base + code_at<D>(t, o), a.k + off, at >= 0);
+                    copy_async<16>(base + kSpan * S::kRow + code_at<D>(t, o), a.v + off, at >= 0);
+                }
+                const int at = max(next_slot, 0);
+                const int64_t off = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
+                                    a.page_size * S::kRow + (at & (a.page_size - 1)) * S::kScales;
+                const uint32_t sc = base + 2 * kSpan * S::kRow + lane * S::kScales;
+                copy_async<S::kScales>(sc, a.k + off, next_slot >= 0);
+                copy_async<S::kScales>(sc + kSpan * S::kScales, a.v + off, next_slot >= 0);
+                if constexpr (kList) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, next_slot >= 0);
+                    if (lane == stage) seen = m;
+                }
+            }
+            ptx::cp_async_commit();
+            resolve();
+        };
+
         resolve();
-    };
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) issue(s);
+        int load_stage = S::kStages - 1, stage = 0;
 
-    resolve();
+        // ---- rows
+        while (more) {
+            // q of row g of every 8, as f16 fragments; a bf16 row is scaled so that its
+            // largest element lies in [2^14, 2^15)
+            uint32_t qf[NT][kElems / 2];
+            float fac[NT][2];  // of rows 2c and 2c + 1: what the scores are multiplied by
+            int limit[NT][2];  // dense: tokens that the row's position sees
 #pragma unroll
-    for (int s = 0; s < S::kStages - 1; ++s) issue(s);
-    int load_stage = S::kStages - 1, stage = 0;
-
-    // ---- rows
-    while (more) {
-        // q of rows g and g + 8 of every 16, as f16 fragments; a bf16 row is scaled
-        // so that its largest element lies in [2^14, 2^15)
-        uint32_t qf[MT][2][kSteps * 2];
-        float fac[MT][2];
-        int limit[MT][2];  // dense: tokens that the row's position sees
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = row0 + mt * 16 + g + 8 * e;
-                const bool in = r < a.rows;
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = row0 + nt * 8 + g;
                 const int n = kList ? draft : min(r / a.group, a.next_n - 1);
-                const int h = hk * a.group + (kList ? r : r % a.group);
-                limit[mt][e] = min(max(w.ctx - a.next_n + 1 + n, 0), w.ctx);
+                const int h = hk * a.group + (kList ? r : r - n * a.group);
                 uint4 raw[kElems / 8];
                 const T* q = static_cast<const T*>(a.q) + (int64_t)w.b * a.q_sb + (int64_t)n * a.q_sn +
                              (int64_t)h * a.q_sh + c * kElems;
 #pragma unroll
                 for (int i = 0; i < kElems / 8; ++i)
-                    raw[i] = in ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+                    raw[i] = r < a.rows ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
                 const uint32_t* wds = reinterpret_cast<const uint32_t*>(raw);
+                float down = a.scale_log2;
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     uint32_t most = 0;  // |x| bits compare like integers
 #pragma unroll
@@ -350,245 +376,238 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttentionA
                     // exponent of the largest, kept where 2^(14 - e) is a normal fp32
                     const int ex = most == 0 ? 14 : max((int)(most >> 7) - 127, -100);
                     const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-                    fac[mt][e] = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+                    down *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
 #pragma unroll
                     for (int i = 0; i < kElems / 2; ++i)
-                        qf[mt][e][i] = pack_f16(__uint_as_float(wds[i] << 16) * up,
-                                                __uint_as_float(wds[i] & 0xffff0000u) * up);
+                        qf[nt][i] = pack_f16(__uint_as_float(wds[i] << 16) * up,
+                                             __uint_as_float(wds[i] & 0xffff0000u) * up);
                 } else {
-                    fac[mt][e] = a.scale_log2;
 #pragma unroll
-                    for (int i = 0; i < kElems / 2; ++i) qf[mt][e][i] = wds[i];
+                    for (int i = 0; i < kElems / 2; ++i) qf[nt][i] = wds[i];
+                }
+                const int sees = min(max(w.ctx - a.next_n + 1 + n, 0), w.ctx);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    fac[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
+                    limit[nt][j] = __shfl_sync(0xffffffffu, sees, 4 * (2 * c + j));
                 }
             }
-        }
 
-        float o[MT][kTiles][4], sum[MT][4], m[MT][2], lraw[MT][2];
+            float o[NT][kTiles][4], sum[NT][4], m[NT][2], lraw[NT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j)
+                for (int i = 0; i < 4; ++i) {
+                    sum[nt][i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[mt][i] = 0.f;
-            m[mt][0] = m[mt][1] = kUnset;
-            lraw[mt][0] = lraw[mt][1] = 0.f;
-        }
+                    for (int j = 0; j < kTiles; ++j) o[nt][j][i] = 0.f;
+                }
+                m[nt][0] = m[nt][1] = kUnset;
+                lraw[nt][0] = lraw[nt][1] = 0.f;
+            }
 
-        for (int t = w.t0 + warp * kSpan; t < w.t1; t += kWarps * kSpan) {
-            ptx::cp_async_wait<S::kStages - 2>();
-            __syncwarp();
-            // which of the chunk's tokens rows g and g + 8 see
-            uint32_t sees[MT][2];
-            bool all;
-            if constexpr (kList) {
-                const uint32_t s = __shfl_sync(0xffffffffu, seen, stage);
-                all = s == 0xffffffffu;
+            for (int t = w.t0 + warp * kSpan; t < w.t1; t += kWarps * kSpan) {
+                ptx::cp_async_wait<S::kStages - 2>();
+                __syncwarp();
+                // which of the span's tokens rows 2c and 2c + 1 see
+                uint32_t sees[NT][2];
+                bool all;
+                if constexpr (kList) {
+                    const uint32_t s = __shfl_sync(0xffffffffu, seen, stage);
+                    all = s == 0xffffffffu;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) sees[mt][0] = sees[mt][1] = s;
-            } else {
-                all = t + kSpan <= min(w.t1, w.ctx - a.next_n + 1);
+                    for (int nt = 0; nt < NT; ++nt) sees[nt][0] = sees[nt][1] = s;
+                } else {
+                    all = t + kSpan <= min(w.t1, w.ctx - a.next_n + 1);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int n = min(max(limit[nt][j] - t, 0), kSpan);
+                            sees[nt][j] = n == 32 ? 0xffffffffu : (1u << n) - 1;
+                        }
+                }
+                issue(load_stage);
+                load_stage = load_stage + 1 == S::kStages ? 0 : load_stage + 1;
+                const uint32_t kc = ring + stage * S::kSlot, vc = kc + kSpan * S::kRow;
+                const uint32_t ks = vc + kSpan * S::kRow, vs = ks + kSpan * S::kScales;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    // ---- scores of 16 tokens: this lane's are g and g + 8
+                    float x[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+                    uint32_t kw[2][kElems / 8], s2[2][2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int n = min(max(limit[mt][e] - t, 0), kSpan);
-                        sees[mt][e] = n == 32 ? 0xffffffffu : (1u << n) - 1;
+                        const uint32_t tok = half * 16 + e * 8 + g;
+                        if constexpr (D == 128) {
+                            const uint4 v = lds128(kc + code_at<D>(tok, c * 16));
+                            kw[e][0] = v.x; kw[e][1] = v.y; kw[e][2] = v.z; kw[e][3] = v.w;
+                            const uint32_t h = e4m3x2_to_f16(lds16(ks + tok * 8 + c * 2));
+                            s2[e][0] = __byte_perm(h, h, 0x1010);
+                            s2[e][1] = __byte_perm(h, h, 0x3232);
+                        } else {
+                            const uint2 v = lds64(kc + code_at<D>(tok, c * 8));
+                            kw[e][0] = v.x; kw[e][1] = v.y;
+                            const uint32_t h = e4m3x2_to_f16(lds8(ks + tok * 4 + c));
+                            s2[e][0] = s2[e][1] = __byte_perm(h, h, 0x1010);
+                        }
                     }
-            }
-            issue(load_stage);
-            load_stage = load_stage + 1 == S::kStages ? 0 : load_stage + 1;
-            const uint32_t kc = ring + stage * S::kSlot, vc = kc + kSpan * S::kRow;
-            const uint32_t ks = vc + kSpan * S::kRow, vs = ks + kSpan * S::kScales;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                // ---- scores of 16 tokens
-                float x[MT][2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint32_t tok = half * 16 + n * 8 + g;
-                    uint32_t kw[kElems / 8], s2[kElems / 16];
-                    if constexpr (D == 128) {
-                        const uint4 v = lds128(kc + code_at<D>(tok, c * 16));
-                        kw[0] = v.x; kw[1] = v.y; kw[2] = v.z; kw[3] = v.w;
-                        const uint32_t h = e4m3x2_to_f16(lds16(ks + tok * 8 + c * 2));
-                        s2[0] = __byte_perm(h, h, 0x1010);
-                        s2[1] = __byte_perm(h, h, 0x3232);
-                    } else {
-                        const uint2 v = lds64(kc + code_at<D>(tok, c * 8));
-                        kw[0] = v.x; kw[1] = v.y;
-                        const uint32_t h = e4m3x2_to_f16(lds8(ks + tok * 4 + c));
-                        s2[0] = __byte_perm(h, h, 0x1010);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[mt][n][i] = 0.f;
 #pragma unroll
                     for (int i = 0; i < kElems / 8; ++i) {
-                        uint32_t f[4];
-                        e2m1_to_f16(kw[i], f);
+                        uint32_t f[2][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) f[k] = mul_f16x2(f[k], s2[i / 2]);
+                        for (int e = 0; e < 2; ++e) {
+                            e2m1_to_f16(kw[e][i], f[e]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) f[e][k] = mul_f16x2(f[e][k], s2[e][i / 2]);
+                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt)
-                                mma16816(x[mt][n], qf[mt][0][4 * i + 2 * k], qf[mt][1][4 * i + 2 * k],
-                                         qf[mt][0][4 * i + 2 * k + 1], qf[mt][1][4 * i + 2 * k + 1],
-                                         f[2 * k], f[2 * k + 1]);
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(x[nt], f[0][2 * k], f[1][2 * k], f[0][2 * k + 1], f[1][2 * k + 1],
+                                         qf[nt][4 * i + 2 * k], qf[nt][4 * i + 2 * k + 1]);
                     }
-                }
-                // ---- y: the scores in base 2, less m
-                float y[MT][2][4];
-                auto scores = [&](int mt, float m0, float m1) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    // ---- y: the scores in base 2, less m
+                    float y[NT][4];
+                    auto scores = [&](int nt, float m0, float m1) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int e = i >> 1;
-                            y[mt][n][i] = fmaf(x[mt][n][i], fac[mt][e], e ? -m1 : -m0);
-                            if (!all && !((sees[mt][e] >> (half * 16 + n * 8 + 2 * c + (i & 1))) & 1))
-                                y[mt][n][i] = -INFINITY;
+                            y[nt][i] = fmaf(x[nt][i], fac[nt][i & 1], i & 1 ? -m1 : -m0);
+                            if (!all && !((sees[nt][i & 1] >> (half * 16 + (i >> 1) * 8 + g)) & 1))
+                                y[nt][i] = -INFINITY;
                         }
-                };
-                bool raise = false;
+                    };
+                    bool raise = false;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    scores(mt, m[mt][0], m[mt][1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        scores(nt, m[nt][0], m[nt][1]);
+                        raise |= fmaxf(fmaxf(y[nt][0], y[nt][1]), fmaxf(y[nt][2], y[nt][3])) > kSlack;
+                    }
+                    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) raise |= fmaxf(y[mt][0][i], y[mt][1][i]) > kSlack;
-                }
-                if (__any_sync(0xffffffffu, raise)) {
+                        for (int nt = 0; nt < NT; ++nt) {
+                            scores(nt, 0.f, 0.f);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        scores(mt, 0.f, 0.f);
+                            for (int j = 0; j < 2; ++j) {
+                                float to = fmaxf(y[nt][j], y[nt][j + 2]);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float to = fmaxf(fmaxf(y[mt][0][2 * e], y[mt][0][2 * e + 1]),
-                                             fmaxf(y[mt][1][2 * e], y[mt][1][2 * e + 1]));
-                            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 1));
-                            to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, 2));
-                            to = fmaxf(to, m[mt][e]);
-                            const float by = ex2(m[mt][e] - to);
-                            m[mt][e] = to;
+                                for (int d = 4; d < 32; d <<= 1)
+                                    to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+                                to = fmaxf(to, m[nt][j]);
+                                const float by = ex2(m[nt][j] - to);
+                                m[nt][j] = to;
 #pragma unroll
-                            for (int j = 0; j < kTiles; ++j) {
-                                o[mt][j][2 * e] *= by;
-                                o[mt][j][2 * e + 1] *= by;
+                                for (int i = 0; i < kTiles; ++i) {
+                                    o[nt][i][j] *= by;
+                                    o[nt][i][j + 2] *= by;
+                                }
+                                sum[nt][j] *= by;
+                                lraw[nt][j] *= by;
                             }
-                            sum[mt][2 * e] *= by;
-                            sum[mt][2 * e + 1] *= by;
-                            lraw[mt][e] *= by;
+                            scores(nt, m[nt][0], m[nt][1]);
                         }
-                        scores(mt, m[mt][0], m[mt][1]);
                     }
-                }
-                uint32_t pf[MT][4];
+                    uint32_t pf[NT][2];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            y[mt][n][i] = ex2(y[mt][n][i]);
-                            lraw[mt][i >> 1] += y[mt][n][i];
+                            y[nt][i] = ex2(y[nt][i]);
+                            lraw[nt][i & 1] += y[nt][i];
                         }
-                        pf[mt][2 * n] = pack_f16(y[mt][n][0], y[mt][n][1]);
-                        pf[mt][2 * n + 1] = pack_f16(y[mt][n][2], y[mt][n][3]);
+                        pf[nt][0] = transpose8(pack_f16(y[nt][0], y[nt][1]));
+                        pf[nt][1] = transpose8(pack_f16(y[nt][2], y[nt][3]));
+                        // the sums of the rounded p, by rows of ones
+                        mma16816(sum[nt], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pf[nt][0], pf[nt][1]);
                     }
-                    // the sum of the rounded p, by a column of ones
-                    mma16816(sum[mt], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], 0x3c003c00u,
-                             0x3c003c00u);
-                }
-                // ---- O += P V: tokens 2c, 2c+1 and 2c+8, 2c+9, elements [g D/8, (g+1) D/8)
-                uint32_t vw[4][D / 64], vsc[2];
+                    // ---- O^T += V^T P^T: tokens 2c, 2c+1 and 2c+8, 2c+9, elements [g D/8, (g+1) D/8)
+                    uint32_t vw[4][D / 64], vsc[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t tok = half * 16 + 2 * c + (e & 1) + 8 * (e >> 1);
-                    if constexpr (D == 128) {
-                        const uint2 v = lds64(vc + code_at<D>(tok, g * 8));
-                        vw[e][0] = v.x; vw[e][1] = v.y;
-                    } else {
-                        vw[e][0] = lds32(vc + code_at<D>(tok, g * 4));
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t tok = half * 16 + 2 * c + (e & 1) + 8 * (e >> 1);
+                        if constexpr (D == 128) {
+                            const uint2 v = lds64(vc + code_at<D>(tok, g * 8));
+                            vw[e][0] = v.x; vw[e][1] = v.y;
+                        } else {
+                            vw[e][0] = lds32(vc + code_at<D>(tok, g * 4));
+                        }
                     }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t at = vs + (half * 16 + 2 * c + 8 * e) * S::kScales + (D == 128 ? g : g / 2);
-                    vsc[e] = e4m3x2_to_f16(lds8(at) | lds8(at + S::kScales) << 8);
-                }
-#pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
-                    // bytes of (token, next token) code pairs, even and odd elements
-                    uint32_t f[2][2][4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t lo = vw[2 * e][i], hi = vw[2 * e + 1][i];
-                        e2m1_to_f16((lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u), f[e][0]);
-                        e2m1_to_f16(((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u), f[e][1]);
+                        const uint32_t at = vs + (half * 16 + 2 * c + 8 * e) * S::kScales + (D == 128 ? g : g / 2);
+                        vsc[e] = e4m3x2_to_f16(lds8(at) | lds8(at + S::kScales) << 8);
                     }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t b0 = mul_f16x2(f[0][k & 1][k >> 1], vsc[0]);
-                        const uint32_t b1 = mul_f16x2(f[1][k & 1][k >> 1], vsc[1]);
+                    for (int i = 0; i < D / 64; ++i) {
+                        // bytes of (token, next token) code pairs, even and odd elements
+                        uint32_t f[2][2][4];
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            mma16816(o[mt][8 * i + k], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], b0, b1);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t lo = vw[2 * e][i], hi = vw[2 * e + 1][i];
+                            e2m1_to_f16((lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u), f[e][0]);
+                            e2m1_to_f16(((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u), f[e][1]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t a0 = mul_f16x2(f[0][0][k], vsc[0]), a1 = mul_f16x2(f[0][1][k], vsc[0]);
+                            const uint32_t a2 = mul_f16x2(f[1][0][k], vsc[1]), a3 = mul_f16x2(f[1][1][k], vsc[1]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(o[nt][4 * i + k], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        }
                     }
                 }
+                stage = stage + 1 == S::kStages ? 0 : stage + 1;
+                __syncwarp();
             }
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
-            __syncwarp();
-        }
 
-        // ---- the CTA's warps join their results; whole rows are written, others left as partials
-        bool whole;
-        int slot;
-        if constexpr (kList) {
-            whole = a.splits == 1;
-            slot = blockIdx.x;
-        } else {
-            whole = w.t0 == 0 && w.t1 == w.ctx;
-            slot = 2 * (int)blockIdx.x + (w.t0 > 0 ? 0 : 1);
-        }
+            // ---- the CTA's warps join their results; whole rows are written, others left as partials
+            bool whole;
+            int64_t slot;
+            if constexpr (kList) {
+                whole = a.splits == 1;
+                slot = (int64_t)w.item * a.splits + part;
+            } else {
+                whole = w.t0 == 0 && w.t1 == w.ctx;
+                slot = 2 * part + (w.t0 > 0 ? 0 : 1);
+            }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r_first = row0 + mt * 16;
-            if (r_first >= a.rows) break;
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float l = lraw[mt][e];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                float* at = red + ((warp * 16 + g + 8 * e) * 4 + c) * S::kLane;
+                for (int j = 0; j < 2; ++j) {
+                    float l = lraw[nt][j];
 #pragma unroll
-                for (int j = 0; j < kTiles; j += 4) {
-                    *reinterpret_cast<float4*>(at + j) =
-                        make_float4(o[mt][j][2 * e], o[mt][j + 1][2 * e], o[mt][j + 2][2 * e], o[mt][j + 3][2 * e]);
-                    *reinterpret_cast<float4*>(at + kTiles + j) =
-                        make_float4(o[mt][j][2 * e + 1], o[mt][j + 1][2 * e + 1], o[mt][j + 2][2 * e + 1], o[mt][j + 3][2 * e + 1]);
+                    for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+                    const int row = warp * S::kRows + nt * 8 + 2 * c + j;
+                    float* at = red + row * S::kRedRow + g * S::kLane;
+#pragma unroll
+                    for (int i = 0; i < kTiles; i += 2)
+                        *reinterpret_cast<float4*>(at + 2 * i) =
+                            make_float4(o[nt][i][j], o[nt][i][j + 2], o[nt][i + 1][j], o[nt][i + 1][j + 2]);
+                    if (g == 0)
+                        *reinterpret_cast<float4*>(red_ml + row * 4) = make_float4(m[nt][j], sum[nt][j], l, 0.f);
                 }
-                if (c == 0)
-                    *reinterpret_cast<float4*>(red_ml + (warp * 16 + g + 8 * e) * 4) =
-                        make_float4(m[mt][e], sum[mt][2 * e], l, 0.f);
             }
             __syncthreads();
-            for (int i = threadIdx.x; i < 16 * (D / 4); i += kThreads) {
-                const int rr = i / (D / 4), d = i % (D / 4) * 4, r = r_first + rr;
+            for (int i = threadIdx.x; i < S::kRows * (D / 4); i += kThreads) {
+                const int rr = i / (D / 4), d = i % (D / 4) * 4, r = row0 + rr;
                 if (r >= a.rows) break;
                 float top = kUnset;
 #pragma unroll
-                for (int k = 0; k < kWarps; ++k) top = fmaxf(top, red_ml[(k * 16 + rr) * 4]);
+                for (int k = 0; k < kWarps; ++k) top = fmaxf(top, red_ml[(k * S::kRows + rr) * 4]);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 float total = 0.f, raw = 0.f;
 #pragma unroll
                 for (int k = 0; k < kWarps; ++k) {
-                    const float4 ml = *reinterpret_cast<const float4*>(red_ml + (k * 16 + rr) * 4);
+                    const float4 ml = *reinterpret_cast<const float4*>(red_ml + (k * S::kRows + rr) * 4);
                     const float by = ex2(ml.x - top);
                     const float4 p = *reinterpret_cast<const float4*>(
-                        red + ((k * 16 + rr) * 4 + d / kElems) * S::kLane + d % kElems);
+                        red + (k * S::kRows + rr) * S::kRedRow + d / (D / 8) * S::kLane + d % (D / 8));
                     v.x = fmaf(p.x, by, v.x);
                     v.y = fmaf(p.y, by, v.y);
                     v.z = fmaf(p.z, by, v.z);
@@ -604,22 +623,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttentionA
                         make_uint2(pack<T>(v.x * inv, v.y * inv), pack<T>(v.z * inv, v.w * inv));
                     if (a.lse != nullptr && d == 0) a.lse[at] = lse_of(top, raw);
                 } else {
-                    const int64_t at = ((int64_t)slot * a.kv_heads + hk) * a.rows + r;
+                    const int64_t at = (slot * a.kv_heads + hk) * a.rows + r;
                     *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
                     if (d == 0) *reinterpret_cast<float4*>(a.part_ml + at * 4) = make_float4(top, total, raw, 0.f);
                 }
             }
             __syncthreads();
-        }
 
-        if constexpr (kList) {
-            more = false;
-        } else {
-            ++w.b;
-            more = settle(a, w, 0);
+            if constexpr (kList) {
+                more = false;
+            } else {
+                ++w.b;
+                more = settle(a, w, 0);
+            }
         }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } while (pair < pairs_end && !kList);
 }
 
 // ---------------------------------------------------------------- combine
@@ -641,17 +660,20 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     const int item = inside ? (int)(id / per_item) : 0;
     const int hr = (int)(id - (int64_t)item * per_item);  // hk * rows + r
 
-    // the CTAs first .. last hold the row's partials
+    const int hk = hr / a.rows, r = hr - hk * a.rows;
+
+    // ranges first .. last (parts of the list) hold the row's partials
     int first = 0, last = -1;
     if constexpr (kList) {
-        first = item * a.splits;
-        last = first + a.splits - 1;
+        last = a.splits - 1;
     } else {
-        // the schedule's entries at or before the row's first unit, and at or before its
-        // last: warp-wide counts (the entries ascend)
+        // the head's ranges that begin at or before the row's first token, and at or
+        // before its last: warp-wide counts (they ascend)
         const int ctx = row_ctx<kList>(a, item);
         int at = 0, upto = 0;
-        for (int i = lane; i < a.num_ctas; i += 32) {
+        for (int k = lane;; k += 32) {
+            const int i = range_start(hk, k, a.kv_heads, a.num_ctas);
+            if (i >= a.num_ctas) break;
             const int b = __ldg(a.schedule + 2 * i), u = __ldg(a.schedule + 2 * i + 1);
             at += b < item || (b == item && u <= 0);
             upto += b < item || (b == item && (int64_t)u * kUnit < ctx);
@@ -670,7 +692,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     float top = kUnset, total = 0.f, raw = 0.f, v[kV] = {};
     if (work) {
         for (int i = first + sub; i <= last; i += wpr) {
-            const int64_t slot = kList ? i : (i == first ? 2 * (int64_t)i + 1 : 2 * (int64_t)i);
+            const int64_t slot = kList ? (int64_t)item * a.splits + i
+                                       : 2 * (int64_t)range_start(hk, i, a.kv_heads, a.num_ctas) + (i == first);
             const int64_t at = slot * per_item + hr;
             const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + at * 4);
             float p[kV];
@@ -707,7 +730,6 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
         }
     }
     if (!work) return;
-    const int hk = hr / a.rows, r = hr - hk * a.rows;
     const int n = kList ? item % a.next_n : r / a.group;
     const int b = kList ? item / a.next_n : item;
     const int64_t at = ((int64_t)b * a.next_n + n) * a.heads + hk * a.group + (kList ? r : r - n * a.group);
@@ -718,18 +740,19 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     if (a.lse != nullptr && lane == 0) a.lse[at] = lse_of(top, raw);
 }
 
-template <int D, int MT, typename T, bool kList>
+template <int D, int NT, typename T, bool kList>
 cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
+    using S = Shape<D, NT>;
     static uint32_t done[64];
-    cudaError_t e = allow_smem(attention_kernel<D, MT, T, kList>, device, Shape<D>::kSmem, done);
+    cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList>, device, S::kSmem, done);
     if (e != cudaSuccess) return e;
-    const int groups = (a.rows + 16 * MT - 1) / (16 * MT);
-    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits : a.num_ctas;
-    e = launch_pdl(attention_kernel<D, MT, T, kList>, dim3((unsigned)x, a.kv_heads * groups),
-                   dim3(kThreads), Shape<D>::kSmem, stream, pdl, a);
-    if (e != cudaSuccess || (kList && a.splits == 1)) return e;
+    const int groups = (a.rows + S::kRows - 1) / S::kRows;
     const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
-    const int64_t parts = kList ? a.splits : (a.num_ctas + a.batch - 1) / a.batch + 1;
+    const int64_t x = kList ? items * a.splits * a.kv_heads : a.num_ctas;
+    e = launch_pdl(attention_kernel<D, NT, T, kList>, dim3((unsigned)x, groups), dim3(S::kThreads),
+                   S::kSmem, stream, pdl, a);
+    if (e != cudaSuccess || (kList && a.splits == 1)) return e;
+    const int64_t parts = kList ? a.splits : (a.num_ctas + a.batch * a.kv_heads - 1) / (a.batch * a.kv_heads) + 1;
     int wpr = 1;
     while (wpr < 8 && wpr * 4 < parts) wpr *= 2;
     const int64_t rows = items * a.kv_heads * a.rows;
@@ -737,14 +760,17 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
                       dim3(kCombineThreads), 0, stream, pdl, a, wpr);
 }
 
+template <int D, int NT, typename T>
+cudaError_t launch_kind(int device, const AttentionArgs& a, void* stream, bool pdl) {
+    return a.topk > 0 ? launch_as<D, NT, T, true>(device, a, stream, pdl)
+                      : launch_as<D, NT, T, false>(device, a, stream, pdl);
+}
+
 template <int D, typename T>
 cudaError_t launch_rows(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    const bool two = a.rows > 16;
-    if (a.topk > 0)
-        return two ? launch_as<D, 2, T, true>(device, a, stream, pdl)
-                   : launch_as<D, 1, T, true>(device, a, stream, pdl);
-    return two ? launch_as<D, 2, T, false>(device, a, stream, pdl)
-               : launch_as<D, 1, T, false>(device, a, stream, pdl);
+    if (a.rows <= 8) return launch_kind<D, 1, T>(device, a, stream, pdl);
+    if (a.rows <= 16) return launch_kind<D, 2, T>(device, a, stream, pdl);
+    return launch_kind<D, 4, T>(device, a, stream, pdl);
 }
 
 }  // namespace

@@ -29,16 +29,16 @@ struct AttentionArgs {
     int32_t topk, splits;     // selected: list length, CTAs per list
 };
 
-// CTAs that share one list of `topk` tokens: enough for two CTAs on every SM,
-// at most one per 256 entries (a CTA's 8 warps take 32 tokens each at a time).
+// CTAs that share one list of `topk` tokens: enough for a CTA on every SM, at most
+// one per 256 entries (8 of a CTA's warps, 32 tokens each).
 inline int topk_splits(int64_t lists, int topk, int sms) {
-    int64_t s = (2 * (int64_t)sms + lists - 1) / lists;
+    int64_t s = sms / (lists > 0 ? lists : 1);
     const int64_t most = (topk + 255) / 256;
     if (s > most) s = most;
     return s < 1 ? 1 : (int)s;
 }
 
-// Slots of partial results: dense, two per CTA of the schedule (the row it
+// Slots of partial results: dense, two per part of the schedule (the row it
 // starts inside of, the row it ends inside of); selected, one per CTA.
 inline int64_t attention_slots(const AttentionArgs& a) {
     if (a.topk == 0) return 2 * (int64_t)a.num_ctas;
