@@ -13,17 +13,11 @@
 // The query rows are N, so 8 rows cost 8 and not 16. At the end of a row the CTA's
 // warps join their (m, sum, O) through shared memory; rows that several CTAs share
 // leave partial results, which combine_kernel joins.
-#include "common.cuh"
-
-#include "attention.cuh"
+#include "attention_walk.cuh"
 #include "host.cuh"
 
 namespace mqa {
 namespace {
-
-constexpr int kSpan = 32;         // tokens of a ring slot
-constexpr float kUnset = -1e30f;  // m of a row that has seen no token
-constexpr float kSlack = 8.f;     // p <= 2^8
 
 // NT: query rows of a CTA / 8. More rows take more registers, so fewer warps.
 template <int D, int NT>
@@ -43,12 +37,6 @@ struct Shape {
     static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // d += a (16 x 16) * b (16 x 8), f16 operands, fp32 accumulation.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -64,140 +52,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-// Eight e2m1 codes as four f16 pairs; byte i becomes pair i (low nibble first).
-__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&o)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return h;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// 16 or 8 bytes global -> shared; zeros where `take` is false (nothing is read).
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool take) {
-    const int bytes = take ? N : 0;
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
-                     ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t v;
-    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-
-// Where a ring slot keeps byte `o` of token t's codes: rows are permuted (and, for
-// 64-byte rows, their 16-byte pieces) so that the K fragments' reads (8 tokens,
-// 16 or 8 bytes a lane) and the V fragments' (tokens 2c of the four lanes of a
-// quad) each touch every bank once.
-template <int D>
-__device__ __forceinline__ uint32_t code_at(uint32_t t, uint32_t o) {
-    if constexpr (D == 128)
-        return (t ^ ((t >> 1) & 1)) * 64 + (o ^ ((t & 4) << 3));
-    else
-        return (t ^ ((t >> 2) & 1)) * 32 + o;
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        return pack_f16(a, b);
-    }
-}
-
-// 2^top * sum as a natural logarithm; -inf where nothing was summed.
-__device__ __forceinline__ float lse_of(float top, float sum) {
-    return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
-}
-
-// A CTA's walk over its rows and over this warp's chunks of them. Dense: the
-// schedule's range; selected: one part of one list.
-struct Walk {
-    int b, last_b, last_u;  // row, and where the CTA's range ends
-    int item;               // the row's index for q and out: b, or b * next_n + n (selected)
-    int ctx;                // tokens of the row (dense), visible tokens (selected)
-    int t0, t1;             // the CTA's tokens (list entries) of this row
-};
-
-template <bool kList>
-__device__ __forceinline__ int row_ctx(const AttentionArgs& a, int b) {
-    return clamp_len(a.status, __ldg(a.context_lens + b), a.max_pages << a.ps_shift);
-}
-
-// Dense: the first row at or after w.b that has tokens in this CTA's range,
-// starting at unit u0 of row w.b. False: none left.
-__device__ __forceinline__ bool settle(const AttentionArgs& a, Walk& w, int u0) {
-    while (w.b < a.batch && (w.b < w.last_b || (w.b == w.last_b && u0 < w.last_u))) {
-        w.ctx = row_ctx<false>(a, w.b);
-        const int units = (w.ctx + kUnit - 1) / kUnit;
-        const int u1 = w.b == w.last_b ? min(units, w.last_u) : units;
-        if (u0 < u1) {
-            w.item = w.b;
-            w.t0 = u0 * kUnit;
-            w.t1 = min(u1 * kUnit, w.ctx);
-            return true;
-        }
-        ++w.b;
-        u0 = 0;
-    }
-    return false;
-}
-
-// The parts of the schedule that CTA i of a dense launch takes: with Hk kv heads the
-// Hk * S (head, part) pairs are dealt in order, Hk to each CTA, so that a CTA walks
-// up to Hk neighbouring parts of one head as one range and rows are cut S + Hk
-// times over all heads. Range k of head hk begins at part range_start(hk, k).
-__host__ __device__ inline int range_start(int hk, int k, int heads, int S) {
-    const int first = (int)(((int64_t)hk * S) % heads);  // parts of the head in its first CTA: heads - first
-    return k == 0 ? 0 : min(S, k * heads - first);
 }
 
 template <int D, int NT, typename T, bool kList>
@@ -217,137 +71,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
     ptx::griddep_wait();
 
     if constexpr (!kList) {
-        if ((a.status.flags & MQA_FLAG_VALIDATE) && blockIdx.y == 0 && warp == 0) {
-            KernelArgs ka{};
-            ka.context_lens = a.context_lens;
-            ka.schedule = a.schedule;
-            ka.status = a.status.caller;
-            ka.lib_status = a.status.lib;
-            ka.batch = a.batch;
-            ka.num_ctas = a.num_ctas;
-            check_schedule(ka, blockIdx.x, lane);
-        }
-        // rows without tokens are in no CTA's range: their results are written here
-        for (int b = blockIdx.x; b < a.batch; b += a.num_ctas) {
-            if (__ldg(a.context_lens + b) > 0) continue;
-            const int64_t o = (int64_t)b * a.next_n * a.heads;
-            for (int j = threadIdx.x; j < a.next_n * a.heads * (D / 8); j += kThreads)
-                reinterpret_cast<uint4*>(a.out)[o * (D / 8) + j] = make_uint4(0, 0, 0, 0);
-            if (a.lse != nullptr)
-                for (int j = threadIdx.x; j < a.next_n * a.heads; j += kThreads) a.lse[o + j] = -INFINITY;
-        }
+        if (blockIdx.y == 0) dense_extras<D>(a, warp, lane);
     }
 
-    int pair = kList ? 0 : blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
+    int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
     const int pairs_end = pair + a.kv_heads;
     do {
-        // ---- one range of rows of one kv head
-        Walk w;
-        int draft = 0, part = 0, hk;
-        bool more;
-        if constexpr (kList) {
-            hk = blockIdx.x % a.kv_heads;
-            const int x = blockIdx.x / a.kv_heads;
-            w.item = x / a.splits;
-            part = x - w.item * a.splits;
-            w.b = w.item / a.next_n;
-            draft = w.item - w.b * a.next_n;
-            const int full = row_ctx<kList>(a, w.b);
-            w.ctx = min(max(full - a.next_n + 1 + draft, 0), full);
-            const int per = ((a.topk + a.splits - 1) / a.splits + kSpan - 1) / kSpan * kSpan;
-            w.t0 = min(a.topk, part * per);
-            w.t1 = min(a.topk, w.t0 + per);
-            more = true;
-        } else {
-            hk = pair / a.num_ctas;
-            part = pair - hk * a.num_ctas;
-            const int n = min(a.num_ctas - part, pairs_end - pair);
-            pair += n;
-            w.b = max(__ldg(a.schedule + 2 * part), 0);
-            const int u0 = max(__ldg(a.schedule + 2 * part + 1), 0);
-            w.last_b = __ldg(a.schedule + 2 * (part + n));
-            w.last_u = __ldg(a.schedule + 2 * (part + n) + 1);
-            more = settle(a, w, u0);
-        }
-
-        // ---- loads: a walk that runs ahead of the computation by kStages - 1 spans
-        Walk lw = w;
-        bool lmore = more;
-        int lpos = lw.t0 + warp * kSpan;  // next span to resolve
-        // The cache slot (page * page_size + slot) of this lane's token of the next
-        // span, -1 for none, found one step before its copies are issued.
-        int next_slot = -1;
-        bool next_any = false;            // the span exists
-        const int32_t* list = kList ? a.indices + (int64_t)w.item * a.topk : nullptr;
-
-        auto resolve = [&]() {
-            next_any = false;
-            next_slot = -1;
-            if constexpr (kList) {
-                if (lpos >= lw.t1) return;
-            } else {
-                while (lmore && lpos >= lw.t1) {
-                    ++lw.b;
-                    lmore = settle(a, lw, 0);
-                    lpos = lw.t0 + warp * kSpan;
-                }
-                if (!lmore) return;
-            }
-            next_any = true;
-            int t = lpos + lane;
-            lpos += kWarps * kSpan;
-            bool ok = t < lw.t1;
-            if constexpr (kList) {
-                t = ok ? __ldg(list + t) : -1;
-                ok = t >= 0 && t < lw.ctx;
-            }
-            if (ok) {
-                int page = __ldg(a.block_table + (int64_t)lw.b * a.max_pages + (t >> a.ps_shift));
-                if (page < 0 || page >= a.num_pages) {
-                    report_checked(a.status, MQA_STATUS_BAD_PAGE);
-                    page = page < 0 ? 0 : a.num_pages - 1;
-                }
-                next_slot = (page << a.ps_shift) | (t & (a.page_size - 1));
-            }
-        };
-
-        const int64_t head_at = (int64_t)hk * a.page_size * (S::kRow + S::kScales);
-        uint32_t seen = 0;  // selected: lane s keeps the mask of the visible tokens in ring slot s
-        auto issue = [&](int stage) {
-            if (next_any) {
-                const uint32_t base = ring + stage * S::kSlot;
-                constexpr int kPieces = S::kRow / 16;       // 16-byte pieces of a token's codes
+        Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
+        const Walk& w = r.w;
+        const int hk = r.hk, draft = r.draft;
+        SpanLoader<D, kWarps * kSpan, kList, false> loads;
+        loads.open(a, r, lane, warp * kSpan);
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
-                    const int at = __shfl_sync(0xffffffffu, next_slot, t);
-                    const int64_t off = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
-                                        (max(at, 0) & (a.page_size - 1)) * S::kRow + o;
-                    copy_async<16>(base + code_at<D>(t, o), a.k + off, at >= 0);
-                    copy_async<16>(base + kSpan * S::kRow + code_at<D>(t, o), a.v + off, at >= 0);
-                }
-                const int at = max(next_slot, 0);
-                const int64_t off = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
-                                    a.page_size * S::kRow + (at & (a.page_size - 1)) * S::kScales;
-                const uint32_t sc = base + 2 * kSpan * S::kRow + lane * S::kScales;
-                copy_async<S::kScales>(sc, a.k + off, next_slot >= 0);
-                copy_async<S::kScales>(sc + kSpan * S::kScales, a.v + off, next_slot >= 0);
-                if constexpr (kList) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, next_slot >= 0);
-                    if (lane == stage) seen = m;
-                }
-            }
-            ptx::cp_async_commit();
-            resolve();
-        };
-
-        resolve();
-#pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) issue(s);
+        for (int s = 0; s < S::kStages - 1; ++s) loads.issue(a, ring + s * S::kSlot, s);
         int load_stage = S::kStages - 1, stage = 0;
 
         // ---- rows
-        while (more) {
+        while (r.more) {
             // q of row g of every 8, as f16 fragments; a bf16 row is scaled so that its
             // largest element lies in [2^14, 2^15)
             uint32_t qf[NT][kElems / 2];
@@ -355,15 +95,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             int limit[NT][2];  // dense: tokens that the row's position sees
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int r = row0 + nt * 8 + g;
-                const int n = kList ? draft : min(r / a.group, a.next_n - 1);
-                const int h = hk * a.group + (kList ? r : r - n * a.group);
+                const int row = row0 + nt * 8 + g;
+                const int n = kList ? draft : min(row / a.group, a.next_n - 1);
+                const int h = hk * a.group + (kList ? row : row - n * a.group);
                 uint4 raw[kElems / 8];
                 const T* q = static_cast<const T*>(a.q) + (int64_t)w.b * a.q_sb + (int64_t)n * a.q_sn +
                              (int64_t)h * a.q_sh + c * kElems;
 #pragma unroll
                 for (int i = 0; i < kElems / 8; ++i)
-                    raw[i] = r < a.rows ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
+                    raw[i] = row < a.rows ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
                 const uint32_t* wds = reinterpret_cast<const uint32_t*>(raw);
                 float down = a.scale_log2;
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -373,10 +113,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                         most = max(most, max(wds[i] & 0x7fffu, (wds[i] >> 16) & 0x7fffu));
                     most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
                     most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    // exponent of the largest, kept where 2^(14 - e) is a normal fp32
-                    const int ex = most == 0 ? 14 : max((int)(most >> 7) - 127, -100);
-                    const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-                    down *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+                    float up, back;
+                    q_power(most, up, back);
+                    down *= back;
 #pragma unroll
                     for (int i = 0; i < kElems / 2; ++i)
                         qf[nt][i] = pack_f16(__uint_as_float(wds[i] << 16) * up,
@@ -413,7 +152,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                 uint32_t sees[NT][2];
                 bool all;
                 if constexpr (kList) {
-                    const uint32_t s = __shfl_sync(0xffffffffu, seen, stage);
+                    const uint32_t s = __shfl_sync(0xffffffffu, loads.seen, stage);
                     all = s == 0xffffffffu;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) sees[nt][0] = sees[nt][1] = s;
@@ -427,7 +166,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                             sees[nt][j] = n == 32 ? 0xffffffffu : (1u << n) - 1;
                         }
                 }
-                issue(load_stage);
+                loads.issue(a, ring + load_stage * S::kSlot, load_stage);
                 load_stage = load_stage + 1 == S::kStages ? 0 : load_stage + 1;
                 const uint32_t kc = ring + stage * S::kSlot, vc = kc + kSpan * S::kRow;
                 const uint32_t ks = vc + kSpan * S::kRow, vs = ks + kSpan * S::kScales;
@@ -567,15 +306,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             }
 
             // ---- the CTA's warps join their results; whole rows are written, others left as partials
-            bool whole;
             int64_t slot;
-            if constexpr (kList) {
-                whole = a.splits == 1;
-                slot = (int64_t)w.item * a.splits + part;
-            } else {
-                whole = w.t0 == 0 && w.t1 == w.ctx;
-                slot = 2 * part + (w.t0 > 0 ? 0 : 1);
-            }
+            const bool whole = row_is_whole<kList>(a, r, slot);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -595,8 +327,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             }
             __syncthreads();
             for (int i = threadIdx.x; i < S::kRows * (D / 4); i += kThreads) {
-                const int rr = i / (D / 4), d = i % (D / 4) * 4, r = row0 + rr;
-                if (r >= a.rows) break;
+                const int rr = i / (D / 4), d = i % (D / 4) * 4, row = row0 + rr;
+                if (row >= a.rows) break;
                 float top = kUnset;
 #pragma unroll
                 for (int k = 0; k < kWarps; ++k) top = fmaxf(top, red_ml[(k * S::kRows + rr) * 4]);
@@ -616,26 +348,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                     raw = fmaf(ml.z, by, raw);
                 }
                 if (whole) {
-                    const int n = kList ? draft : r / a.group;
-                    const int64_t at = ((int64_t)w.b * a.next_n + n) * a.heads + hk * a.group + (kList ? r : r - n * a.group);
+                    const int n = kList ? draft : row / a.group;
+                    const int64_t at = ((int64_t)w.b * a.next_n + n) * a.heads + hk * a.group + (kList ? row : row - n * a.group);
                     const float inv = total == 0.f ? 0.f : 1.f / total;
                     *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * D + d) =
                         make_uint2(pack<T>(v.x * inv, v.y * inv), pack<T>(v.z * inv, v.w * inv));
                     if (a.lse != nullptr && d == 0) a.lse[at] = lse_of(top, raw);
                 } else {
-                    const int64_t at = (slot * a.kv_heads + hk) * a.rows + r;
+                    const int64_t at = (slot * a.kv_heads + hk) * a.rows + row;
                     *reinterpret_cast<float4*>(a.part_o + at * D + d) = v;
                     if (d == 0) *reinterpret_cast<float4*>(a.part_ml + at * 4) = make_float4(top, total, raw, 0.f);
                 }
             }
             __syncthreads();
 
-            if constexpr (kList) {
-                more = false;
-            } else {
-                ++w.b;
-                more = settle(a, w, 0);
-            }
+            next_row<kList>(a, r);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } while (pair < pairs_end && !kList);
@@ -669,7 +396,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     } else {
         // the head's ranges that begin at or before the row's first token, and at or
         // before its last: warp-wide counts (they ascend)
-        const int ctx = row_ctx<kList>(a, item);
+        const int ctx = row_ctx(a, item);
         int at = 0, upto = 0;
         for (int k = lane;; k += 32) {
             const int i = range_start(hk, k, a.kv_heads, a.num_ctas);
@@ -687,7 +414,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
         last = upto - 1;
     }
     bool work = inside;
-    if constexpr (!kList) work = work && last > first && row_ctx<kList>(a, item) > 0;
+    if constexpr (!kList) work = work && last > first && row_ctx(a, item) > 0;
 
     float top = kUnset, total = 0.f, raw = 0.f, v[kV] = {};
     if (work) {
@@ -741,17 +468,25 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
 }
 
 template <int D, int NT, typename T, bool kList>
-cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
+cudaError_t launch_narrow(int device, const AttentionArgs& a, void* stream, bool pdl) {
     using S = Shape<D, NT>;
     static uint32_t done[64];
-    cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList>, device, S::kSmem, done);
+    const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList>, device, S::kSmem, done);
     if (e != cudaSuccess) return e;
     const int groups = (a.rows + S::kRows - 1) / S::kRows;
-    const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
-    const int64_t x = kList ? items * a.splits * a.kv_heads : a.num_ctas;
-    e = launch_pdl(attention_kernel<D, NT, T, kList>, dim3((unsigned)x, groups), dim3(S::kThreads),
-                   S::kSmem, stream, pdl, a);
+    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
+    return launch_pdl(attention_kernel<D, NT, T, kList>, dim3((unsigned)x, groups), dim3(S::kThreads),
+                      S::kSmem, stream, pdl, a);
+}
+
+template <int D, typename T, bool kList>
+cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
+    const cudaError_t e = a.rows <= 8    ? launch_narrow<D, 1, T, kList>(device, a, stream, pdl)
+                          : a.rows <= 16 ? launch_narrow<D, 2, T, kList>(device, a, stream, pdl)
+                          : a.rows <= 32 ? launch_narrow<D, 4, T, kList>(device, a, stream, pdl)
+                                         : launch_wide<D, T, kList>(device, a, stream, pdl);
     if (e != cudaSuccess || (kList && a.splits == 1)) return e;
+    const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
     const int64_t parts = kList ? a.splits : (a.num_ctas + a.batch * a.kv_heads - 1) / (a.batch * a.kv_heads) + 1;
     int wpr = 1;
     while (wpr < 8 && wpr * 4 < parts) wpr *= 2;
@@ -760,17 +495,10 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
                       dim3(kCombineThreads), 0, stream, pdl, a, wpr);
 }
 
-template <int D, int NT, typename T>
-cudaError_t launch_kind(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    return a.topk > 0 ? launch_as<D, NT, T, true>(device, a, stream, pdl)
-                      : launch_as<D, NT, T, false>(device, a, stream, pdl);
-}
-
 template <int D, typename T>
 cudaError_t launch_rows(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    if (a.rows <= 8) return launch_kind<D, 1, T>(device, a, stream, pdl);
-    if (a.rows <= 16) return launch_kind<D, 2, T>(device, a, stream, pdl);
-    return launch_kind<D, 4, T>(device, a, stream, pdl);
+    return a.topk > 0 ? launch_as<D, T, true>(device, a, stream, pdl)
+                      : launch_as<D, T, false>(device, a, stream, pdl);
 }
 
 }  // namespace

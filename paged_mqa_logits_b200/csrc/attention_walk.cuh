@@ -1,0 +1,344 @@
+// Device pieces that the attention kernels share: number formats, the walk over a
+// CTA's ranges of rows, and the asynchronous copies of 32 tokens at a time.
+#pragma once
+#include "common.cuh"
+
+#include "attention.cuh"
+
+namespace mqa {
+
+constexpr int kSpan = 32;         // tokens of a ring slot
+constexpr float kUnset = -1e30f;  // m of a row that has seen no token
+constexpr float kSlack = 8.f;     // p <= 2^8
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Eight e2m1 codes as four f16 pairs; byte i becomes pair i (low nibble first).
+__device__ __forceinline__ void e2m1_to_f16(uint32_t w, uint32_t (&o)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 16 or 8 bytes global -> shared; zeros where `take` is false (nothing is read).
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool take) {
+    const int bytes = take ? N : 0;
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
+                     ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// Where a ring slot keeps byte `o` of token t's codes: rows are permuted (and, for
+// 64-byte rows, their 16-byte pieces) so that the K fragments' reads (8 tokens,
+// 16 or 8 bytes a lane) and the V fragments' (tokens 2c of the four lanes of a
+// quad) each touch every bank once.
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t t, uint32_t o) {
+    if constexpr (D == 128)
+        return (t ^ ((t >> 1) & 1)) * 64 + (o ^ ((t & 4) << 3));
+    else
+        return (t ^ ((t >> 2) & 1)) * 32 + o;
+}
+
+// The same where a lane reads its own token's codes, 16 bytes at a time.
+template <int D>
+__device__ __forceinline__ uint32_t tile_at(uint32_t t, uint32_t o) {
+    if constexpr (D == 128)
+        return t * 64 + (o ^ ((t << 3) & 48));
+    else
+        return t * 32 + (o ^ ((t << 2) & 16));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_f16(a, b);
+    }
+}
+
+// 2^top * sum as a natural logarithm; -inf where nothing was summed.
+__device__ __forceinline__ float lse_of(float top, float sum) {
+    return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+}
+
+// A CTA's walk over its rows and over this warp's chunks of them. Dense: the
+// schedule's range; selected: one part of one list.
+struct Walk {
+    int b, last_b, last_u;  // row, and where the CTA's range ends
+    int item;               // the row's index for q and out: b, or b * next_n + n (selected)
+    int ctx;                // tokens of the row (dense), visible tokens (selected)
+    int t0, t1;             // the CTA's tokens (list entries) of this row
+};
+
+__device__ __forceinline__ int row_ctx(const AttentionArgs& a, int b) {
+    return clamp_len(a.status, __ldg(a.context_lens + b), a.max_pages << a.ps_shift);
+}
+
+// Dense: the first row at or after w.b that has tokens in this CTA's range,
+// starting at unit u0 of row w.b. False: none left.
+__device__ __forceinline__ bool settle(const AttentionArgs& a, Walk& w, int u0) {
+    while (w.b < a.batch && (w.b < w.last_b || (w.b == w.last_b && u0 < w.last_u))) {
+        w.ctx = row_ctx(a, w.b);
+        const int units = (w.ctx + kUnit - 1) / kUnit;
+        const int u1 = w.b == w.last_b ? min(units, w.last_u) : units;
+        if (u0 < u1) {
+            w.item = w.b;
+            w.t0 = u0 * kUnit;
+            w.t1 = min(u1 * kUnit, w.ctx);
+            return true;
+        }
+        ++w.b;
+        u0 = 0;
+    }
+    return false;
+}
+
+// The parts of the schedule that CTA i of a dense launch takes: with Hk kv heads the
+// Hk * S (head, part) pairs are dealt in order, Hk to each CTA, so that a CTA walks
+// up to Hk neighbouring parts of one head as one range and rows are cut S + Hk
+// times over all heads. Range k of head hk begins at part range_start(hk, k).
+__host__ __device__ inline int range_start(int hk, int k, int heads, int S) {
+    const int first = (int)(((int64_t)hk * S) % heads);  // parts of the head in its first CTA: heads - first
+    return k == 0 ? 0 : min(S, k * heads - first);
+}
+
+
+// One range of rows of one kv head (dense), or one part of one list.
+struct Range {
+    Walk w;
+    int hk, part, draft;
+    bool more;
+};
+
+// Dense: opens the range at (head, part) pair `pair` and moves `pair` behind it.
+// Selected: the part of the list that CTA x of the grid takes.
+template <bool kList>
+__device__ __forceinline__ Range open_range(const AttentionArgs& a, int x, int& pair, int pairs_end) {
+    Range r;
+    Walk& w = r.w;
+    if constexpr (kList) {
+        r.hk = x % a.kv_heads;
+        const int y = x / a.kv_heads;
+        w.item = y / a.splits;
+        r.part = y - w.item * a.splits;
+        w.b = w.item / a.next_n;
+        r.draft = w.item - w.b * a.next_n;
+        const int full = row_ctx(a, w.b);
+        w.ctx = min(max(full - a.next_n + 1 + r.draft, 0), full);
+        const int per = ((a.topk + a.splits - 1) / a.splits + kSpan - 1) / kSpan * kSpan;
+        w.t0 = min(a.topk, r.part * per);
+        w.t1 = min(a.topk, w.t0 + per);
+        w.last_b = w.b;
+        w.last_u = 0;
+        r.more = true;
+    } else {
+        r.draft = 0;
+        r.hk = pair / a.num_ctas;
+        r.part = pair - r.hk * a.num_ctas;
+        const int n = min(a.num_ctas - r.part, pairs_end - pair);
+        pair += n;
+        w.b = max(__ldg(a.schedule + 2 * r.part), 0);
+        const int u0 = max(__ldg(a.schedule + 2 * r.part + 1), 0);
+        w.last_b = __ldg(a.schedule + 2 * (r.part + n));
+        w.last_u = __ldg(a.schedule + 2 * (r.part + n) + 1);
+        r.more = settle(a, w, u0);
+    }
+    return r;
+}
+
+// Moves a range to its next row.
+template <bool kList>
+__device__ __forceinline__ void next_row(const AttentionArgs& a, Range& r) {
+    if constexpr (kList) {
+        r.more = false;
+    } else {
+        ++r.w.b;
+        r.more = settle(a, r.w, 0);
+    }
+}
+
+// Where the row's result goes: complete, or which partial slot.
+template <bool kList>
+__device__ __forceinline__ bool row_is_whole(const AttentionArgs& a, const Range& r, int64_t& slot) {
+    if constexpr (kList) {
+        slot = (int64_t)r.w.item * a.splits + r.part;
+        return a.splits == 1;
+    } else {
+        slot = 2 * r.part + (r.w.t0 > 0 ? 0 : 1);
+        return r.w.t0 == 0 && r.w.t1 == r.w.ctx;
+    }
+}
+
+// What every dense launch does besides: the schedule's check in validate mode, and
+// the results of rows without tokens, which are in no CTA's range.
+template <int D>
+__device__ __forceinline__ void dense_extras(const AttentionArgs& a, int warp, int lane) {
+    if ((a.status.flags & MQA_FLAG_VALIDATE) && warp == 0) {
+        KernelArgs ka{};
+        ka.context_lens = a.context_lens;
+        ka.schedule = a.schedule;
+        ka.status = a.status.caller;
+        ka.lib_status = a.status.lib;
+        ka.batch = a.batch;
+        ka.num_ctas = a.num_ctas;
+        check_schedule(ka, blockIdx.x, lane);
+    }
+    for (int b = blockIdx.x; b < a.batch; b += a.num_ctas) {
+        if (__ldg(a.context_lens + b) > 0) continue;
+        const int64_t o = (int64_t)b * a.next_n * a.heads;
+        for (int j = threadIdx.x; j < a.next_n * a.heads * (D / 8); j += blockDim.x)
+            reinterpret_cast<uint4*>(a.out)[o * (D / 8) + j] = make_uint4(0, 0, 0, 0);
+        if (a.lse != nullptr)
+            for (int j = threadIdx.x; j < a.next_n * a.heads; j += blockDim.x) a.lse[o + j] = -INFINITY;
+    }
+}
+
+// A warp's loads, running ahead of its computation: kStep tokens from one span of 32
+// to the warp's next, `off` its place in them. kTile: every warp has a span wherever
+// the step has a token (zeros behind the row); else only where the span has one.
+template <int D, int kStep, bool kList, bool kTile>
+struct SpanLoader {
+    static constexpr int kRow = D / 2, kScales = D / 16;
+    Range r;
+    const int32_t* list;
+    int64_t head_at;
+    int lane, off, pos;
+    int slot;       // this lane's token's cache slot (page * page_size + slot), -1 for none,
+    bool any;       // of the span to be copied next, if there is one: found a step ahead
+    uint32_t seen;  // selected: lane s keeps the mask of the visible tokens in ring slot s
+
+    __device__ __forceinline__ void open(const AttentionArgs& a, const Range& range, int lane_, int off_) {
+        r = range;
+        lane = lane_;
+        off = off_;
+        pos = r.w.t0 + off;
+        list = kList ? a.indices + (int64_t)r.w.item * a.topk : nullptr;
+        head_at = (int64_t)r.hk * a.page_size * (kRow + kScales);
+        seen = 0;
+        resolve(a);
+    }
+
+    __device__ __forceinline__ void resolve(const AttentionArgs& a) {
+        any = false;
+        slot = -1;
+        while (r.more && (kTile ? pos - off : pos) >= r.w.t1) {
+            next_row<kList>(a, r);
+            pos = r.w.t0 + off;
+        }
+        if (!r.more) return;
+        any = true;
+        int t = pos + lane;
+        pos += kStep;
+        bool ok = t < r.w.t1;
+        if constexpr (kList) {
+            t = ok ? __ldg(list + t) : -1;
+            ok = t >= 0 && t < r.w.ctx;
+        }
+        if (ok) {
+            int page = __ldg(a.block_table + (int64_t)r.w.b * a.max_pages + (t >> a.ps_shift));
+            if (page < 0 || page >= a.num_pages) {
+                report_checked(a.status, MQA_STATUS_BAD_PAGE);
+                page = page < 0 ? 0 : a.num_pages - 1;
+            }
+            slot = (page << a.ps_shift) | (t & (a.page_size - 1));
+        }
+    }
+
+    // Copies the span into ring slot `base` (number `stage`): K codes, V codes, K
+    // scales, V scales, zeros where there is no token; one copy group, empty if none.
+    __device__ __forceinline__ void issue(const AttentionArgs& a, uint32_t base, int stage) {
+        if (any) {
+            constexpr int kPieces = kRow / 16;  // 16-byte pieces of a token's codes
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
+                const int at = __shfl_sync(0xffffffffu, slot, t);
+                const int64_t from = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
+                                     (max(at, 0) & (a.page_size - 1)) * kRow + o;
+                const uint32_t to = kTile ? tile_at<D>(t, o) : code_at<D>(t, o);
+                copy_async<16>(base + to, a.k + from, at >= 0);
+                copy_async<16>(base + kSpan * kRow + to, a.v + from, at >= 0);
+            }
+            const int at = max(slot, 0);
+            const int64_t from = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
+                                 a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
+            const uint32_t sc = base + 2 * kSpan * kRow + lane * kScales;
+            copy_async<kScales>(sc, a.k + from, slot >= 0);
+            copy_async<kScales>(sc + kSpan * kScales, a.v + from, slot >= 0);
+            if constexpr (kList) {
+                const uint32_t m = __ballot_sync(0xffffffffu, slot >= 0);
+                if (lane == stage) seen = m;
+            }
+        }
+        ptx::cp_async_commit();
+        resolve(a);
+    }
+};
+
+// The power of two that a row of q is multiplied by (its bits `most`: the largest |x|
+// of a bf16 row), so that its largest element lies in [2^14, 2^15), and what undoes it.
+__device__ __forceinline__ void q_power(uint32_t most, float& up, float& down) {
+    // kept where both are normal fp32
+    const int ex = most == 0 ? 14 : max((int)(most >> 7) - 127, -100);
+    up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+    down = __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+}
+
+}  // namespace mqa
