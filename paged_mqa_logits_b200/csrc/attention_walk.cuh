@@ -9,7 +9,7 @@ namespace mqa {
 
 constexpr int kSpan = 32;         // tokens of a ring slot
 constexpr float kUnset = -1e30f;  // m of a row that has seen no token
-constexpr float kSlack = 8.f;     // p <= 2^8
+constexpr float kSlack = 15.f;    // p <= 2^15, within f16; the largest p is at least 1
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -299,6 +299,27 @@ struct SpanLoader {
             }
             slot = (page << a.ps_shift) | (t & (a.page_size - 1));
         }
+    }
+
+    // The same for one of the two caches: its codes, then its scales.
+    __device__ __forceinline__ void issue_one(const AttentionArgs& a, const uint8_t* cache, uint32_t base) {
+        if (any) {
+            constexpr int kPieces = kRow / 16;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
+                const int at = __shfl_sync(0xffffffffu, slot, t);
+                const int64_t from = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
+                                     (max(at, 0) & (a.page_size - 1)) * kRow + o;
+                copy_async<16>(base + (kTile ? tile_at<D>(t, o) : code_at<D>(t, o)), cache + from, at >= 0);
+            }
+            const int at = max(slot, 0);
+            const int64_t from = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
+                                 a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
+            copy_async<kScales>(base + kSpan * kRow + lane * kScales, cache + from, slot >= 0);
+        }
+        ptx::cp_async_commit();
+        resolve(a);
     }
 
     // Copies the span into ring slot `base` (number `stage`): K codes, V codes, K

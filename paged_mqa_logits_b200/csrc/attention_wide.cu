@@ -3,18 +3,22 @@
 //
 // A tile is 128 tokens. S = Q K^T (M = 128 query rows, N = 128 tokens) with Q in
 // TMEM and K, dequantised to f16, in shared memory; P = 2^(S - m) goes back to TMEM
-// over S, and O += P V with P as the A operand from TMEM and V in shared memory
+// again, and O += P V with P as the A operand from TMEM and V in shared memory
 // (tokens are the contraction, so V is the MN-major operand and needs no
 // transpose). Rows are TMEM lanes, so maxima and sums of a row need no exchange but
 // the one between the two warps that share a row's columns.
 //
-// Warps: 0-7 softmax (warp w: rows 32 (w % 4).., columns 64 (w / 4)..), 8-11
-// dequantise (32 tokens of each tile, through a ring of asynchronous copies of
-// their own), 12 issues the MMAs. S, K and V have two buffers each; S of the next
-// tile is issued ahead of the current tile's O.
+// Warps: 0 issues S and 1 O; 4-7 and 8-11 softmax (a warp has 32 rows; the two
+// groups take tiles in turn, so that one group's exponentials run while the other's
+// products do), 12-15 dequantise K and 16-19 V (32 tokens of each tile, through rings
+// of asynchronous copies of their own). S, K and V have two buffers each.
 //
-// m is raised, and O rescaled, only when a score exceeds it by kSlack (see
-// attention.cu). All waits are bounded: on a timeout the status word gets
+// m is raised, by whole numbers so that every rescaling is exact, only when a score
+// exceeds it by kSlack (see attention.cu). A tile is computed with the m that its
+// group knows; at its end the group learns the m that O has by then (`ref`, settled
+// in turn, tile by tile) and scales whichever of P and O is behind, which is rare. So
+// a tile needs one pass over S, and the groups wait for each other only where one
+// of them is late. All waits are bounded: on a timeout the status word gets
 // MQA_STATUS_TIMEOUT and every role leaves.
 #include "attention_walk.cuh"
 #include "host.cuh"
@@ -24,22 +28,27 @@ namespace {
 
 constexpr int kTokens = 128;       // of a tile
 constexpr int kSoftmaxWarps = 8;
-constexpr int kDequantWarps = 4;
-constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
-constexpr int kWideThreads = 32 * (kMmaWarp + 1);
+constexpr int kDequantWarps = 4;   // for each of K and V
+// First warps: 0 issues S, 1 issues O (the lowest numbers, since the hardware prefers
+// older warps and everything waits for these two; 2 and 3 keep the others' places
+// in their quarters of TMEM), then the softmax and the dequantising warps.
+constexpr int kMmaWarp = 0, kSoftmaxWarp = 4, kDequantWarp = kSoftmaxWarp + kSoftmaxWarps;
+constexpr int kWideThreads = 32 * (kDequantWarp + 2 * kDequantWarps);
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-// TMEM columns: two S buffers (P over their first halves), O, Q.
-constexpr int kColS = 0, kColO = 256, kColQ = 384, kColumns = 512;
+// TMEM columns: two S buffers of 128 (P over their second halves), O, Q.
+constexpr int kColS = 0, kColP = 64, kColO = 256, kColQ = 384, kColumns = 512;
+constexpr uint32_t kTmem = 0;  // where an allocation of all 512 columns begins
 
 template <int D>
 struct Wide {
     static constexpr int kRow = D / 2, kScales = D / 16;
-    static constexpr int kSlot = 2 * kSpan * (kRow + kScales);
+    static constexpr int kSlot = kSpan * (kRow + kScales);
     static constexpr int kStages = 4;
     static constexpr int kBuf = kTokens * D * 2;  // a tile of K or V: [D / 64][128 tokens][64] f16, 128-byte swizzle
     static constexpr int kK = 0, kV = 2 * kBuf, kRing = 4 * kBuf;
-    static constexpr int kExch = kRing + kDequantWarps * kStages * kSlot;  // [2][2][128] fp32
-    static constexpr int kBars = kExch + 2 * 2 * 128 * 4;
+    static constexpr int kExch = kRing + 2 * kDequantWarps * kStages * kSlot;  // [2][2][128] fp32
+    static constexpr int kRef = kExch + 2 * 2 * 128 * 4;                       // [128] fp32: m of each row
+    static constexpr int kBars = kRef + 128 * 4;
     static constexpr int kSmem = kBars + 256 + 1024;  // slack for aligning the base
     static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
 };
@@ -47,37 +56,56 @@ struct Wide {
 struct Bars {
     uint64_t k_full[2], v_full[2];  // the dequantising warps arrive
     uint64_t s_full[2];             // S computed (and its K buffer free)
-    uint64_t p_full[2];             // the softmax warps arrive
-    uint64_t pv_done[2];            // O updated (S and V buffers free)
+    uint64_t p_full[2];             // a group's warps arrive: P written
+    uint64_t pv_done[2];            // O updated (S, P and V buffers free)
     uint64_t q_full;                // the softmax warps arrive: a row's Q is in TMEM
-    uint64_t pair[4];               // the two warps of a row quarter
-    uint64_t drain;
+    uint64_t turn[4][2];            // a row quarter's m is settled for the tile
+    uint64_t pair[4];               // the two warps of a row quarter exchange values
+    uint64_t drain[2];
     int32_t abort;
     uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
-// Waits for phase `parity`, taken by lane 0 for the warp. False: give up.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, Bars* bars,
-                                           const StatusWords& st, int lane) {
-    bool ok = true;
-    if (lane == 0 && !ptx::mbar_try_wait(bar, parity)) {
-        const uint64_t t0 = ptx::globaltimer();
-        volatile int32_t* abort = &bars->abort;
-        while (!ptx::mbar_try_wait_sleep(bar, parity, kWaitSliceNs)) {
-            if (*abort) {
-                ok = false;
-                break;
-            }
-            if (ptx::globaltimer() - t0 > kTimeoutNs) {
-                report(st, MQA_STATUS_TIMEOUT);
-                *abort = 1;
-                ok = false;
-                break;
-            }
+// Waits for phase `parity`, by one thread. False: give up.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Bars* bars, const StatusWords& st) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    volatile int32_t* abort = &bars->abort;
+    while (!ptx::mbar_try_wait_sleep(bar, parity, kWaitSliceNs)) {
+        if (*abort) return false;
+        if (ptx::globaltimer() - t0 > kTimeoutNs) {
+            report(st, MQA_STATUS_TIMEOUT);
+            *abort = 1;
+            return false;
         }
     }
+    return true;
+}
+
+// The same for a warp, which stays together: every lane looks once, lane 0 waits.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, Bars* bars,
+                                           const StatusWords& st, int lane) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    bool ok = true;
+    if (lane == 0) ok = wait_one(bar, parity, bars, st);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], f16 operands, issued by the lane whose `lead` is 1.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(ptx::smem_u32(bar)), "r"(lead) : "memory");
 }
 
 __device__ __forceinline__ void fence_async_smem() {
@@ -88,24 +116,18 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// 64 or 16 consecutive columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_read64(uint32_t taddr, float (&v)[64]) {
+// 32 or 16 consecutive columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, float (&v)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19,"
-        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37,"
-        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55,"
-        "%56, %57, %58, %59, %60, %61, %62, %63}"
-        ", [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
+        ", [%32];\n\ttcgen05.wait::ld.sync.aligned;"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
           "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
           "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]),
           "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]),
-          "=f"(v[29]), "=f"(v[30]), "=f"(v[31]), "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]),
-          "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]), "=f"(v[40]), "=f"(v[41]), "=f"(v[42]),
-          "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]), "=f"(v[48]), "=f"(v[49]),
-          "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]), "=f"(v[56]),
-          "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+          "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tmem_read16(uint32_t taddr, float (&v)[16]) {
@@ -116,6 +138,18 @@ __device__ __forceinline__ void tmem_read16(uint32_t taddr, float (&v)[16]) {
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
           "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 __device__ __forceinline__ int tiles_of(const Walk& w) { return (w.t1 - w.t0 + kTokens - 1) / kTokens; }
@@ -132,11 +166,11 @@ __device__ __forceinline__ void dequant_row(uint32_t codes, uint32_t scales, uin
         sc[0] = lds32(scales + lane * 4);
     }
     const uint32_t line = tile + row * 128;
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < D / 32; ++j) {
         const uint4 v = lds128(codes + tile_at<D>(lane, j * 16));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t h = e4m3x2_to_f16(sc[j / 2] >> ((j & 1) * 16));
+        const uint32_t h = e4m3x2_to_f16((D == 128 && j > 1 ? sc[D / 64 - 1] : sc[0]) >> ((j & 1) * 16));
         const uint32_t s[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -157,6 +191,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     const uint32_t base = ptx::smem_u32(smem);
     float* exch = reinterpret_cast<float*>(smem + W::kExch);
+    float* ref = reinterpret_cast<float*>(smem + W::kRef);
     Bars* bars = reinterpret_cast<Bars*>(smem + W::kBars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -166,19 +201,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
             ptx::mbar_init(&bars->k_full[i], kDequantWarps);
             ptx::mbar_init(&bars->v_full[i], kDequantWarps);
             ptx::mbar_init(&bars->s_full[i], 1);
-            ptx::mbar_init(&bars->p_full[i], kSoftmaxWarps);
+            ptx::mbar_init(&bars->p_full[i], kSoftmaxWarps / 2);
             ptx::mbar_init(&bars->pv_done[i], 1);
+            for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[q][i], 1);
         }
         ptx::mbar_init(&bars->q_full, kSoftmaxWarps);
-        for (int i = 0; i < 4; ++i) ptx::mbar_init(&bars->pair[i], 2);
-        ptx::mbar_init(&bars->drain, 1);
+        for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->pair[q], 2);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
         bars->abort = 0;
         ptx::fence_mbar_init();
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = bars->tmem;
+    constexpr uint32_t tmem = kTmem;
 
     ptx::griddep_wait();
     if constexpr (!kList) dense_extras<D>(a, warp, lane);
@@ -188,123 +224,114 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     int it = 0;                          // tiles so far: buffers and phases go by it
     bool ok = true;
 
-    if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
+    if (warp >= kDequantWarp) {
         // ------------------------------------------------------------ dequantise
-        const int dw = warp - kSoftmaxWarps, row = dw * kSpan + lane;
-        const uint32_t ring = base + W::kRing + dw * (W::kStages * W::kSlot);
+        const bool is_v = warp >= kDequantWarp + kDequantWarps;
+        const int dw = (warp - kDequantWarp) & 3, row = dw * kSpan + lane;
+        const uint32_t ring = base + W::kRing + (warp - kDequantWarp) * (W::kStages * W::kSlot);
+        const uint32_t tiles = base + (is_v ? W::kV : W::kK);
+        uint64_t* const full = is_v ? bars->v_full : bars->k_full;
+        uint64_t* const free = is_v ? bars->pv_done : bars->s_full;
         do {
             Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
             SpanLoader<D, kTokens, kList, true> loads;
             loads.open(a, r, lane, dw * kSpan);
 #pragma unroll
-            for (int s = 0; s < W::kStages - 1; ++s) loads.issue(a, ring + s * W::kSlot, s);
+            for (int s = 0; s < W::kStages - 1; ++s) loads.issue_one(a, is_v ? a.v : a.k, ring + s * W::kSlot);
             int load_stage = W::kStages - 1, stage = 0;
             while (ok && r.more) {
                 const int n = tiles_of(r.w);
                 for (int j = 0; j < n; ++j, ++it) {
                     ptx::cp_async_wait<W::kStages - 2>();
                     __syncwarp();
-                    loads.issue(a, ring + load_stage * W::kSlot, load_stage);
+                    loads.issue_one(a, is_v ? a.v : a.k, ring + load_stage * W::kSlot);
                     load_stage = load_stage + 1 == W::kStages ? 0 : load_stage + 1;
                     const uint32_t slot = ring + stage * W::kSlot;
                     stage = stage + 1 == W::kStages ? 0 : stage + 1;
-                    const uint32_t b = it & 1, before = ((it >> 1) & 1) ^ 1;
-                    ok = wait_phase(&bars->s_full[b], before, bars, a.status, lane);
+                    const uint32_t b = it & 1;
+                    ok = wait_phase(&free[b], ((it >> 1) & 1) ^ 1, bars, a.status, lane);
                     if (!ok) break;
-                    dequant_row<D>(slot, slot + 2 * kSpan * W::kRow, base + W::kK + b * W::kBuf, lane, row);
+                    dequant_row<D>(slot, slot + kSpan * W::kRow, tiles + b * W::kBuf, lane, row);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->k_full[b]);
-                    ok = wait_phase(&bars->pv_done[b], before, bars, a.status, lane);
-                    if (!ok) break;
-                    dequant_row<D>(slot + kSpan * W::kRow, slot + 2 * kSpan * W::kRow + kSpan * W::kScales,
-                                   base + W::kV + b * W::kBuf, lane, row);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->v_full[b]);
+                    if (lane == 0) ptx::mbar_arrive(&full[b]);
                 }
                 next_row<kList>(a, r);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         } while (ok && pair < pairs_end && !kList);
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMAs
-        const uint32_t id_qk = ptx::instr_desc(0, 0, 128, kTokens);
-        const uint32_t id_pv = ptx::instr_desc(0, 0, 128, D) | (1u << 16);  // B is MN-major
-        auto scores = [&](int i) {
-            const uint32_t b = i & 1;
-            if (!wait_phase(&bars->pv_done[b], ((i >> 1) & 1) ^ 1, bars, a.status, lane)) return false;
-            if (!wait_phase(&bars->k_full[b], (i >> 1) & 1, bars, a.status, lane)) return false;
-            ptx::tc_fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t kd = ptx::smem_desc(
-                        base + W::kK + b * W::kBuf + (k >> 2) * (kTokens * 128) + (k & 3) * 32, 16, 1024, ptx::SW_128B);
-                    ptx::mma_f16_ts(tmem + kColS + b * 128, tmem + kColQ + k * 8, kd, id_qk, k > 0);
-                }
-                ptx::tc_commit(&bars->s_full[b]);
-            }
-            __syncwarp();
-            return true;
-        };
+    } else if (warp <= kMmaWarp + 1) {
+        // ------------------------------------------------------------ MMAs: the warp walks, lane 0 issues
+        const bool is_s = warp == kMmaWarp;
+        const uint32_t lead = lane == 0;
+        constexpr uint32_t id_qk = ptx::instr_desc(0, 0, 128, kTokens);
+        constexpr uint32_t id_pv = ptx::instr_desc(0, 0, 128, D) | (1u << 16);  // B is MN-major
+        // K-major: 8-token groups 1024 bytes apart; MN-major: those, and 64-element
+        // pieces of D kTokens * 128 apart. Addresses are in 16-byte units.
+        const uint64_t k0 = ptx::smem_desc(base + W::kK, 16, 1024, ptx::SW_128B);
+        const uint64_t v0 = ptx::smem_desc(base + W::kV, kTokens * 128, 1024, ptx::SW_128B);
         int seg = 0;
         do {
             Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
             while (ok && r.more) {
                 const int n = tiles_of(r.w);
-                if (n > 0) {
-                    ok = wait_phase(&bars->q_full, seg & 1, bars, a.status, lane) && scores(it);
-                    ++seg;
-                }
+                if (is_s && n > 0) ok = wait_phase(&bars->q_full, seg++ & 1, bars, a.status, lane);
                 for (int j = 0; ok && j < n; ++j, ++it) {
-                    if (j + 1 < n) ok = scores(it + 1);
                     const uint32_t b = it & 1, phase = (it >> 1) & 1;
-                    ok = ok && wait_phase(&bars->v_full[b], phase, bars, a.status, lane) &&
-                         wait_phase(&bars->p_full[b], phase, bars, a.status, lane);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    if (lane == 0) {
+                    if (is_s) {
+                        ok = wait_phase(&bars->k_full[b], phase, bars, a.status, lane) &&
+                             wait_phase(&bars->pv_done[b], phase ^ 1, bars, a.status, lane);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint64_t kd = k0 + b * (W::kBuf / 16);
 #pragma unroll
-                        for (int k = 0; k < kTokens / 16; ++k) {
-                            // 64-element pieces of D lie kTokens * 128 bytes apart, 8-token groups 1024
-                            const uint64_t vd = ptx::smem_desc(base + W::kV + b * W::kBuf + k * 2048,
-                                                               kTokens * 128, 1024, ptx::SW_128B);
-                            ptx::mma_f16_ts(tmem + kColO, tmem + kColS + b * 128 + k * 8, vd, id_pv, j > 0 || k > 0);
-                        }
-                        ptx::tc_commit(&bars->pv_done[b]);
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ts(lead, kTmem + kColS + b * 128, kTmem + kColQ + k * 8,
+                                   kd + (k >> 2) * (kTokens * 128 / 16) + (k & 3) * 2, id_qk, k > 0);
+                        commit(lead, &bars->s_full[b]);
+                    } else {
+                        ok = wait_phase(&bars->v_full[b], phase, bars, a.status, lane) &&
+                             wait_phase(&bars->p_full[b], phase, bars, a.status, lane);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        const uint64_t vd = v0 + b * (W::kBuf / 16);
+#pragma unroll
+                        for (int k = 0; k < kTokens / 16; ++k)
+                            mma_ts(lead, kTmem + kColO, kTmem + kColS + b * 128 + kColP + k * 8, vd + k * 128, id_pv,
+                                   j > 0 || k > 0);
+                        commit(lead, &bars->pv_done[b]);
                     }
-                    __syncwarp();
                 }
                 next_row<kList>(a, r);
             }
         } while (ok && pair < pairs_end && !kList);
-        if (lane == 0) {  // nothing of this CTA's MMAs is under way when it ends
-            ptx::tc_commit(&bars->drain);
+        // nothing of this CTA's MMAs is under way when it ends
+        commit(lead, &bars->drain[is_s]);
+        if (lane == 0) {
             const uint64_t t0 = ptx::globaltimer();
-            while (!ptx::mbar_try_wait_sleep(&bars->drain, 0, kWaitSliceNs))
+            while (!ptx::mbar_try_wait_sleep(&bars->drain[is_s], 0, kWaitSliceNs))
                 if (ptx::globaltimer() - t0 > kTimeoutNs) {
                     report(a.status, MQA_STATUS_TIMEOUT);
                     break;
                 }
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kSoftmaxWarp) {
         // ------------------------------------------------------------ softmax
-        const int q4 = warp & 3, half = warp >> 2;
+        const int q4 = warp & 3, group = (warp - kSoftmaxWarp) >> 2;
         const int row = q4 * 32 + lane;
         const bool active = q4 * 32 < a.rows;  // the quarter has query rows
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
         uint32_t swaps = 0;
-        // the other warp's value for this row
+        // the other group's value for this row
         auto swap = [&](float mine, float& other) {
             float* at = exch + (swaps & 1) * 256;
-            at[half * 128 + row] = mine;
+            at[group * 128 + row] = mine;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->pair[q4]);
             const bool got = wait_phase(&bars->pair[q4], swaps & 1, bars, a.status, lane);
-            other = at[(half ^ 1) * 128 + row];
+            other = at[(group ^ 1) * 128 + row];
             ++swaps;
             return got;
         };
@@ -321,10 +348,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 const int limit = min(max(w.ctx - a.next_n + 1 + draft, 0), w.ctx);
                 if (n > 0) {
                     if (active) {
-                        // ---- this half of the row's q to TMEM
+                        // ---- this group's half of the row's q to TMEM
                         uint32_t wds[D / 4];
                         const T* q = static_cast<const T*>(a.q) + (int64_t)w.b * a.q_sb + (int64_t)draft * a.q_sn +
-                                     (int64_t)h * a.q_sh + half * (D / 2);
+                                     (int64_t)h * a.q_sh + group * (D / 2);
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const uint4 v = row < a.rows ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
@@ -353,7 +380,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                         }
 #pragma unroll
                         for (int i = 0; i < D / 64; ++i)
-                            ptx::tmem_st16(lanes + kColQ + half * (D / 4) + 16 * i,
+                            ptx::tmem_st16(lanes + kColQ + group * (D / 4) + 16 * i,
                                            reinterpret_cast<const uint32_t(&)[16]>(wds[16 * i]));
                         ptx::tmem_st_wait();
                     }
@@ -361,95 +388,132 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bars->q_full);
                 }
+                fac = fmaxf(fac, 1e-37f);  // a factor of 0 must not make NaN of an invisible column's -inf
+                const uint64_t fac2 = ptx::f32x2_pack(fac, fac);
+                uint64_t l2 = 0;  // two partial sums of p, relative to m
+                auto scale_l = [&](float by) {
+                    float l0, l1;
+                    ptx::f32x2_unpack(l2, l0, l1);
+                    l2 = ptx::f32x2_pack(l0 * by, l1 * by);
+                };
+                auto scale_p = [&](uint32_t at, float power) {  // 32 columns of P, by 2^power in two steps within f16
+                    ptx::tmem_st_wait();
+                    float p[16];
+                    tmem_read16(at, p);
+                    uint32_t v[16];
+                    const float h = ceilf(0.5f * power), b0 = ex2(h), b1 = ex2(power - h);
+                    const uint32_t by0 = pack_f16(b0, b0), by1 = pack_f16(b1, b1);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = mul_f16x2(mul_f16x2(__float_as_uint(p[k]), by0), by1);
+                    ptx::tmem_st16(at, v);
+                };
                 for (int j = 0; j < n; ++j, ++it) {
-                    const uint32_t b = it & 1, phase = (it >> 1) & 1;
+                    if ((it & 1) != group) continue;
+                    const uint32_t b = group, phase = (it >> 1) & 1;
+                    const uint32_t s_at = lanes + kColS + b * 128, p_at = s_at + kColP;
                     const int t = w.t0 + j * kTokens;
-                    uint32_t sees[2] = {~0u, ~0u};  // the 64 columns that the row sees
+                    uint32_t see0 = ~0u, see1 = ~0u, see2 = ~0u, see3 = ~0u;  // the columns that the row sees
                     bool all;
                     if constexpr (kList) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int e = t + half * 64 + i * 32 + lane;
+                        auto listed = [&](int i) {
+                            const int e = t + i * 32 + lane;
                             const int tok = e < w.t1 ? __ldg(a.indices + (int64_t)w.item * a.topk + e) : -1;
-                            sees[i] = __ballot_sync(0xffffffffu, tok >= 0 && tok < w.ctx);
-                        }
-                        all = (sees[0] & sees[1]) == ~0u;
+                            return __ballot_sync(0xffffffffu, tok >= 0 && tok < w.ctx);
+                        };
+                        see0 = listed(0);
+                        see1 = listed(1);
+                        see2 = listed(2);
+                        see3 = listed(3);
+                        all = (see0 & see1 & see2 & see3) == ~0u;
                     } else {
                         all = t + kTokens <= min(w.t1, w.ctx - a.next_n + 1);
+                        auto upto = [&](int i) {
+                            const int k = min(max(limit - t - i * 32, 0), 32);
+                            return k == 32 ? ~0u : (1u << k) - 1;
+                        };
                         if (!all) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int k = min(max(limit - t - half * 64 - i * 32, 0), 32);
-                                sees[i] = k == 32 ? ~0u : (1u << k) - 1;
-                            }
+                            see0 = upto(0);
+                            see1 = upto(1);
+                            see2 = upto(2);
+                            see3 = upto(3);
                         }
                     }
                     ok = wait_phase(&bars->s_full[b], phase, bars, a.status, lane);
                     if (!ok) break;
                     if (active) {
                         ptx::tc_fence_after();
-                        float s[64];
-                        tmem_read64(lanes + kColS + b * 128 + half * 64, s);
-                        ptx::tc_fence_before();
-                        if (!all) {
+                        // P goes over S from the last columns on: those of S that it takes are
+                        // read by then. A loop of small code: unrolled, the kernel's roles
+                        // together no longer fit the instruction cache.
+#pragma unroll 1
+                        for (int i = 3; i >= 0; --i) {
+                            float s[32];
+                            tmem_read32(s_at + 32 * i, s);
+                            if (!all) {
+                                const uint32_t see = i == 0 ? see0 : i == 1 ? see1 : i == 2 ? see2 : see3;
 #pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (!((sees[i >> 5] >> (i & 31)) & 1)) s[i] = -3e38f;
-                        }
-                        float top[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            top[i] = s[i];
-#pragma unroll
-                            for (int k = 4; k < 64; k += 4) top[i] = fmaxf(top[i], s[k + i]);
-                        }
-                        const float mine = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fac;
-                        float other;
-                        ok = swap(mine, other);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const float most = fmaxf(mine, other);
-                        const bool raise = most > m + kSlack;
-                        if (__any_sync(0xffffffffu, raise)) {
-                            const float by = raise ? ex2(m - most) : 1.f;
-                            if (raise) m = most;
-                            l *= by;
-                            if (j > 0) {
-                                ok = wait_phase(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-#pragma unroll
-                                for (int i = 0; i < D / 32; ++i) {
-                                    float o[16];
-                                    tmem_read16(lanes + kColO + half * (D / 2) + 16 * i, o);
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] *= by;
-                                    ptx::tmem_st16(lanes + kColO + half * (D / 2) + 16 * i,
-                                                   reinterpret_cast<const uint32_t(&)[16]>(o));
-                                }
+                                for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
                             }
-                        }
-                        // P goes over S: the columns of this half's P were read by the other
-                        // warp before the swap
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                            float most[2] = {s[0], s[1]};
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                            for (int k = 2; k < 30; k += 4) {
+                                most[0] = max3(most[0], s[k], s[k + 1]);
+                                most[1] = max3(most[1], s[k + 2], s[k + 3]);
+                            }
+                            most[0] = max3(max3(most[0], s[30], s[31]), most[1], most[1]) * fac;
+                            if (__any_sync(0xffffffffu, most[0] > m + kSlack)) {
+                                const float to = most[0] > m + kSlack ? floorf(most[0]) : m;
+                                scale_l(ex2(m - to));
+#pragma unroll 1
+                                for (int k = 3; k > i; --k) scale_p(p_at + 16 * k, m - to);
+                                m = to;
+                            }
+                            const uint64_t m2 = ptx::f32x2_pack(-m, -m);
                             uint32_t p[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                float e0 = ex2(fmaf(s[32 * i + 2 * k], fac, -m));
-                                float e1 = ex2(fmaf(s[32 * i + 2 * k + 1], fac, -m));
-                                if (!all) {
-                                    if (!((sees[i] >> (2 * k)) & 1)) e0 = 0.f;
-                                    if (!((sees[i] >> (2 * k + 1)) & 1)) e1 = 0.f;
-                                }
-                                sum[2 * (k & 1)] += e0;
-                                sum[2 * (k & 1) + 1] += e1;
+                                float e0, e1;
+                                ptx::f32x2_unpack(ptx::fma_f32x2(ptx::f32x2_pack(s[2 * k], s[2 * k + 1]), fac2, m2), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                l2 = add_f32x2(l2, ptx::f32x2_pack(e0, e1));
                                 p[k] = pack_f16(e0, e1);
                             }
-                            ptx::tmem_st16(lanes + kColS + b * 128 + half * 32 + 16 * i, p);
+                            ptx::tmem_st16(p_at + 16 * i, p);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        // ---- the m that O has after the tile before
+                        if (it > 0) {
+                            ok = wait_phase(&bars->turn[q4][b ^ 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                            if (!ok) break;
+                        }
+                        const float had = j > 0 ? ref[row] : m;
+                        if (__any_sync(0xffffffffu, had != m)) {
+                            const float to = fmaxf(had, m);
+                            if (__any_sync(0xffffffffu, m < to)) {  // P is behind
+                                scale_l(ex2(m - to));
+                                
+#pragma unroll 1
+                                for (int k = 0; k < 4; ++k) scale_p(p_at + 16 * k, m - to);
+                            }
+                            if (__any_sync(0xffffffffu, had < to)) {  // O is behind
+                                ok = wait_phase(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                                if (!ok) break;
+                                ptx::tc_fence_after();
+                                const float by = ex2(had - to);
+#pragma unroll 1
+                                for (int i = 0; i < D / 16; ++i) {
+                                    float o[16];
+                                    tmem_read16(lanes + kColO + 16 * i, o);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] *= by;
+                                    ptx::tmem_st16(lanes + kColO + 16 * i, reinterpret_cast<const uint32_t(&)[16]>(o));
+                                }
+                            }
+                            m = to;
+                        }
+                        if (j == 0 || had != m) ref[row] = m;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&bars->turn[q4][b]);
                         ptx::tmem_st_wait();
                         ptx::tc_fence_before();
                     }
@@ -457,17 +521,26 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     if (lane == 0) ptx::mbar_arrive(&bars->p_full[b]);
                 }
                 if (!ok) break;
-                // ---- the row's result
+                // ---- the row's result: each group has half of its columns
                 if (n > 0) {
                     ok = wait_phase(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
                     if (!ok) break;
                     ptx::tc_fence_after();
                 }
                 if (active) {
+                    if (n > 0) {
+                        ok = wait_phase(&bars->turn[q4][(it - 1) & 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                        if (!ok) break;
+                        const float to = ref[row];  // settled by the last tile
+                        float l0, l1;
+                        ptx::f32x2_unpack(l2, l0, l1);
+                        l = (l0 + l1) * ex2(m - to);
+                        m = to;
+                    }
                     float other;
                     ok = swap(l, other);
                     if (!ok) break;
-                    l += other;
+                    l = group ? other + l : l + other;
                     int64_t slot;
                     const bool whole = row_is_whole<kList>(a, r, slot);
                     const int64_t at_part = (slot * a.kv_heads + r.hk) * a.rows + row;
@@ -475,14 +548,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         float o[16];
+                        const int d = group * (D / 2) + 16 * i;
                         if (n > 0) {
-                            tmem_read16(lanes + kColO + half * (D / 2) + 16 * i, o);
+                            tmem_read16(lanes + kColO + d, o);
                         } else {
 #pragma unroll
                             for (int k = 0; k < 16; ++k) o[k] = 0.f;
                         }
                         if (row < a.rows) {
-                            const int d = half * (D / 2) + 16 * i;
                             if (whole) {
                                 uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at_row * D + d);
                                 uint32_t v[8];
@@ -498,7 +571,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                             }
                         }
                     }
-                    if (row < a.rows && half == 0) {
+                    if (row < a.rows && group == 0) {
                         if (whole) {
                             if (a.lse != nullptr) a.lse[at_row] = lse_of(m, l);
                         } else {
