@@ -1,12 +1,11 @@
 // Attention over the FP4 cache for many query rows a kv head (33 to 128): both
 // products on the 5th-generation tensor core.
 //
-// A tile is 128 tokens. S = Q K^T (M = 128 query rows, N = 128 tokens) with Q in
-// TMEM and K, dequantised to f16, in shared memory; P = 2^(S - m) goes back to TMEM
-// again, and O += P V with P as the A operand from TMEM and V in shared memory
-// (tokens are the contraction, so V is the MN-major operand and needs no
-// transpose). Rows are TMEM lanes, so maxima and sums of a row need no exchange but
-// the one between the two warps that share a row's columns.
+// A tile is 128 tokens. S = Q K^T (M = 128 query rows, N = 128 tokens) with Q and K,
+// dequantised to f16, in shared memory; P = 2^(S - m) goes back to TMEM, and
+// O += P V with P as the A operand from TMEM and V in shared memory (tokens are the
+// contraction, so V is the MN-major operand and needs no transpose). Rows are TMEM
+// lanes: a thread has a row, and maxima and sums need no exchange.
 //
 // Warps: 0 issues S and 1 O; 4-7 and 8-11 softmax (a warp has 32 rows; the two
 // groups take tiles in turn, so that one group's exponentials run while the other's
@@ -35,17 +34,18 @@ constexpr int kDequantWarps = 4;   // for each of K and V
 constexpr int kMmaWarp = 0, kSoftmaxWarp = 4, kDequantWarp = kSoftmaxWarp + kSoftmaxWarps;
 constexpr int kWideThreads = 32 * (kDequantWarp + 2 * kDequantWarps);
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-// TMEM columns: two S buffers of 128 (P over their second halves), O, Q.
-constexpr int kColS = 0, kColP = 64, kColO = 256, kColQ = 384, kColumns = 512;
+// TMEM columns: three S buffers of 128 (P over their second halves), O. With three, S
+// is two tiles ahead and no group waits for a product; Q is in shared memory for it.
+constexpr int kBufS = 3, kColP = 64, kColO = 128 * kBufS, kColumns = 512;
 constexpr uint32_t kTmem = 0;  // where an allocation of all 512 columns begins
 
 template <int D>
 struct Wide {
     static constexpr int kRow = D / 2, kScales = D / 16;
     static constexpr int kSlot = kSpan * (kRow + kScales);
-    static constexpr int kStages = 4;
+    static constexpr int kStages = 3;
     static constexpr int kBuf = kTokens * D * 2;  // a tile of K or V: [D / 64][128 tokens][64] f16, 128-byte swizzle
-    static constexpr int kK = 0, kV = 2 * kBuf, kRing = 4 * kBuf;
+    static constexpr int kK = 0, kV = 2 * kBuf, kQ = 4 * kBuf, kRing = 5 * kBuf;
     static constexpr int kExch = kRing + 2 * kDequantWarps * kStages * kSlot;  // [2][2][128] fp32
     static constexpr int kRef = kExch + 2 * 2 * 128 * 4;                       // [128] fp32: m of each row
     static constexpr int kBars = kRef + 128 * 4;
@@ -55,10 +55,11 @@ struct Wide {
 
 struct Bars {
     uint64_t k_full[2], v_full[2];  // the dequantising warps arrive
-    uint64_t s_full[2];             // S computed (and its K buffer free)
-    uint64_t p_full[2];             // a group's warps arrive: P written
-    uint64_t pv_done[2];            // O updated (S, P and V buffers free)
-    uint64_t q_full;                // the softmax warps arrive: a row's Q is in TMEM
+    uint64_t s_full[kBufS];         // S computed (and its K buffer free)
+    uint64_t p_full[kBufS];         // a group's warps arrive: P written
+    uint64_t s_free[kBufS];         // P used
+    uint64_t pv_done[2];            // O updated (and its V buffer free)
+    uint64_t q_full;                // the softmax warps arrive: Q is in shared memory
     uint64_t turn[4][2];            // a row quarter's m is settled for the tile
     uint64_t pair[4];               // the two warps of a row quarter exchange values
     uint64_t drain[2];
@@ -99,6 +100,15 @@ __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, ui
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
+}
+
+// The same with A from shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead) : "memory");
 }
 
 __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
@@ -200,10 +210,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars->k_full[i], kDequantWarps);
             ptx::mbar_init(&bars->v_full[i], kDequantWarps);
-            ptx::mbar_init(&bars->s_full[i], 1);
-            ptx::mbar_init(&bars->p_full[i], kSoftmaxWarps / 2);
             ptx::mbar_init(&bars->pv_done[i], 1);
             for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[q][i], 1);
+        }
+        for (int i = 0; i < kBufS; ++i) {
+            ptx::mbar_init(&bars->s_full[i], 1);
+            ptx::mbar_init(&bars->p_full[i], kSoftmaxWarps / 2);
+            ptx::mbar_init(&bars->s_free[i], 1);
         }
         ptx::mbar_init(&bars->q_full, kSoftmaxWarps);
         for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->pair[q], 2);
@@ -221,7 +234,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
 
     int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
     const int pairs_end = pair + a.kv_heads;
-    int it = 0;                          // tiles so far: buffers and phases go by it
+    // Tiles so far: buffers and phases go by their number. Tile i is in S buffer i % 3,
+    // for the i / 3-th time.
+    int it = 0;
     bool ok = true;
 
     if (warp >= kDequantWarp) {
@@ -231,7 +246,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         const uint32_t ring = base + W::kRing + (warp - kDequantWarp) * (W::kStages * W::kSlot);
         const uint32_t tiles = base + (is_v ? W::kV : W::kK);
         uint64_t* const full = is_v ? bars->v_full : bars->k_full;
-        uint64_t* const free = is_v ? bars->pv_done : bars->s_full;
         do {
             Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
             SpanLoader<D, kTokens, kList, true> loads;
@@ -249,7 +263,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     const uint32_t slot = ring + stage * W::kSlot;
                     stage = stage + 1 == W::kStages ? 0 : stage + 1;
                     const uint32_t b = it & 1;
-                    ok = wait_phase(&free[b], ((it >> 1) & 1) ^ 1, bars, a.status, lane);
+                    if (it >= 2) {  // the tile before last in this buffer has been used
+                        ok = is_v ? wait_phase(&bars->pv_done[b], ((it >> 1) & 1) ^ 1, bars, a.status, lane)
+                                  : wait_phase(&bars->s_full[(it - 2) % kBufS], (it - 2) / kBufS & 1, bars, a.status, lane);
+                    }
                     if (!ok) break;
                     dequant_row<D>(slot, slot + kSpan * W::kRow, tiles + b * W::kBuf, lane, row);
                     fence_async_smem();
@@ -270,6 +287,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         // K-major: 8-token groups 1024 bytes apart; MN-major: those, and 64-element
         // pieces of D kTokens * 128 apart. Addresses are in 16-byte units.
         const uint64_t k0 = ptx::smem_desc(base + W::kK, 16, 1024, ptx::SW_128B);
+        const uint64_t q0 = ptx::smem_desc(base + W::kQ, 16, 1024, ptx::SW_128B);
         const uint64_t v0 = ptx::smem_desc(base + W::kV, kTokens * 128, 1024, ptx::SW_128B);
         int seg = 0;
         do {
@@ -278,29 +296,30 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 const int n = tiles_of(r.w);
                 if (is_s && n > 0) ok = wait_phase(&bars->q_full, seg++ & 1, bars, a.status, lane);
                 for (int j = 0; ok && j < n; ++j, ++it) {
-                    const uint32_t b = it & 1, phase = (it >> 1) & 1;
+                    const uint32_t b = it & 1, phase = (it >> 1) & 1, sb = it % kBufS, s_phase = it / kBufS & 1;
                     if (is_s) {
                         ok = wait_phase(&bars->k_full[b], phase, bars, a.status, lane) &&
-                             wait_phase(&bars->pv_done[b], phase ^ 1, bars, a.status, lane);
+                             wait_phase(&bars->s_free[sb], s_phase ^ 1, bars, a.status, lane);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         const uint64_t kd = k0 + b * (W::kBuf / 16);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            mma_ts(lead, kTmem + kColS + b * 128, kTmem + kColQ + k * 8,
+                            mma_ss(lead, kTmem + sb * 128, q0 + (k >> 2) * (kTokens * 128 / 16) + (k & 3) * 2,
                                    kd + (k >> 2) * (kTokens * 128 / 16) + (k & 3) * 2, id_qk, k > 0);
-                        commit(lead, &bars->s_full[b]);
+                        commit(lead, &bars->s_full[sb]);
                     } else {
                         ok = wait_phase(&bars->v_full[b], phase, bars, a.status, lane) &&
-                             wait_phase(&bars->p_full[b], phase, bars, a.status, lane);
+                             wait_phase(&bars->p_full[sb], s_phase, bars, a.status, lane);
                         if (!ok) break;
                         ptx::tc_fence_after();
                         const uint64_t vd = v0 + b * (W::kBuf / 16);
 #pragma unroll
                         for (int k = 0; k < kTokens / 16; ++k)
-                            mma_ts(lead, kTmem + kColO, kTmem + kColS + b * 128 + kColP + k * 8, vd + k * 128, id_pv,
+                            mma_ts(lead, kTmem + kColO, kTmem + sb * 128 + kColP + k * 8, vd + k * 128, id_pv,
                                    j > 0 || k > 0);
                         commit(lead, &bars->pv_done[b]);
+                        commit(lead, &bars->s_free[sb]);
                     }
                 }
                 next_row<kList>(a, r);
@@ -348,7 +367,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 const int limit = min(max(w.ctx - a.next_n + 1 + draft, 0), w.ctx);
                 if (n > 0) {
                     if (active) {
-                        // ---- this group's half of the row's q to TMEM
+                        // ---- this group's half of the row's q, where the MMA reads it
                         uint32_t wds[D / 4];
                         const T* q = static_cast<const T*>(a.q) + (int64_t)w.b * a.q_sb + (int64_t)draft * a.q_sn +
                                      (int64_t)h * a.q_sh + group * (D / 2);
@@ -379,11 +398,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                                                   __uint_as_float(wds[i] & 0xffff0000u) * up);
                         }
 #pragma unroll
-                        for (int i = 0; i < D / 64; ++i)
-                            ptx::tmem_st16(lanes + kColQ + group * (D / 4) + 16 * i,
-                                           reinterpret_cast<const uint32_t(&)[16]>(wds[16 * i]));
-                        ptx::tmem_st_wait();
+                        for (int i = 0; i < D / 16; ++i) {
+                            const int u = group * (D / 16) + i;  // 16-byte unit of the row
+                            sts128(base + W::kQ + (u >> 3) * (kTokens * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                                   wds[4 * i], wds[4 * i + 1], wds[4 * i + 2], wds[4 * i + 3]);
+                        }
                     }
+                    fence_async_smem();
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bars->q_full);
@@ -409,8 +430,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 };
                 for (int j = 0; j < n; ++j, ++it) {
                     if ((it & 1) != group) continue;
-                    const uint32_t b = group, phase = (it >> 1) & 1;
-                    const uint32_t s_at = lanes + kColS + b * 128, p_at = s_at + kColP;
+                    const uint32_t b = group, sb = it % kBufS;
+                    const uint32_t s_at = lanes + sb * 128, p_at = s_at + kColP;
                     const int t = w.t0 + j * kTokens;
                     uint32_t see0 = ~0u, see1 = ~0u, see2 = ~0u, see3 = ~0u;  // the columns that the row sees
                     bool all;
@@ -438,7 +459,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                             see3 = upto(3);
                         }
                     }
-                    ok = wait_phase(&bars->s_full[b], phase, bars, a.status, lane);
+                    ok = wait_phase(&bars->s_full[sb], it / kBufS & 1, bars, a.status, lane);
                     if (!ok) break;
                     if (active) {
                         ptx::tc_fence_after();
@@ -501,12 +522,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                                 ptx::tc_fence_after();
                                 const float by = ex2(had - to);
 #pragma unroll 1
-                                for (int i = 0; i < D / 16; ++i) {
-                                    float o[16];
-                                    tmem_read16(lanes + kColO + 16 * i, o);
+                                for (int i = 0; i < D / 32; ++i) {
+                                    float o[32];
+                                    tmem_read32(lanes + kColO + 32 * i, o);
 #pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] *= by;
-                                    ptx::tmem_st16(lanes + kColO + 16 * i, reinterpret_cast<const uint32_t(&)[16]>(o));
+                                    for (int k = 0; k < 32; ++k) o[k] *= by;
+                                    ptx::tmem_st16(lanes + kColO + 32 * i, reinterpret_cast<const uint32_t(&)[16]>(o[0]));
+                                    ptx::tmem_st16(lanes + kColO + 32 * i + 16, reinterpret_cast<const uint32_t(&)[16]>(o[16]));
                                 }
                             }
                             m = to;
@@ -518,7 +540,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                         ptx::tc_fence_before();
                     }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->p_full[b]);
+                    if (lane == 0) ptx::mbar_arrive(&bars->p_full[sb]);
                 }
                 if (!ok) break;
                 // ---- the row's result: each group has half of its columns
