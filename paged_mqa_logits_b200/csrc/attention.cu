@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                 for (int i = 0; i < kElems / 8; ++i)
                     raw[i] = row < a.rows ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
                 const uint32_t* wds = reinterpret_cast<const uint32_t*>(raw);
-                float down = a.scale_log2;
+                float down = fabsf(a.scale_log2);
+                uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale's sign goes into q
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     uint32_t most = 0;  // |x| bits compare like integers
 #pragma unroll
@@ -118,12 +119,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                     down *= back;
 #pragma unroll
                     for (int i = 0; i < kElems / 2; ++i)
-                        qf[nt][i] = pack_f16(__uint_as_float(wds[i] << 16) * up,
-                                             __uint_as_float(wds[i] & 0xffff0000u) * up);
+                        qf[nt][i] = flip ^ pack_f16(__uint_as_float(wds[i] << 16) * up,
+                                                    __uint_as_float(wds[i] & 0xffff0000u) * up);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kElems / 2; ++i) qf[nt][i] = wds[i];
+                    for (int i = 0; i < kElems / 2; ++i) qf[nt][i] = flip ^ wds[i];
                 }
+                down = fmaxf(down, 1e-37f);  // a factor of 0 must not make NaN of an invisible token's -inf
                 const int sees = min(max(w.ctx - a.next_n + 1 + n, 0), w.ctx);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -211,15 +213,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                                 mma16816(x[nt], f[0][2 * k], f[1][2 * k], f[0][2 * k + 1], f[1][2 * k + 1],
                                          qf[nt][4 * i + 2 * k], qf[nt][4 * i + 2 * k + 1]);
                     }
+                    if (!all) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!((sees[nt][i & 1] >> (half * 16 + (i >> 1) * 8 + g)) & 1)) x[nt][i] = -INFINITY;
+                    }
                     // ---- y: the scores in base 2, less m
                     float y[NT][4];
                     auto scores = [&](int nt, float m0, float m1) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 4; ++i)
                             y[nt][i] = fmaf(x[nt][i], fac[nt][i & 1], i & 1 ? -m1 : -m0);
-                            if (!all && !((sees[nt][i & 1] >> (half * 16 + (i >> 1) * 8 + g)) & 1))
-                                y[nt][i] = -INFINITY;
-                        }
                     };
                     bool raise = false;
 #pragma unroll

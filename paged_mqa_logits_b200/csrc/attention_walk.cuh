@@ -55,6 +55,15 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool t
                      ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
 }
 
+// The same of something that is there.
+template <int N>
+__device__ __forceinline__ void copy_async_all(uint32_t dst, const void* src) {
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -301,48 +310,60 @@ struct SpanLoader {
         }
     }
 
-    // The same for one of the two caches: its codes, then its scales.
-    __device__ __forceinline__ void issue_one(const AttentionArgs& a, const uint8_t* cache, uint32_t base) {
-        if (any) {
-            constexpr int kPieces = kRow / 16;
+    // Copies the span's codes and scales of `caches` caches (K, then V, to slots
+    // `stride` apart) into ring slot `base`: rows of codes, scales `scales` behind
+    // them; zeros where there is no token.
+    template <int kCaches>
+    __device__ __forceinline__ void copy(const AttentionArgs& a, const uint8_t* c0, const uint8_t* c1, uint32_t base,
+                                         uint32_t stride, uint32_t scales, uint32_t scale_stride) {
+        constexpr int kPieces = kRow / 16;  // 16-byte pieces of a token's codes
+        auto place = [](int t, int o) { return kTile ? tile_at<D>(t, o) : code_at<D>(t, o); };
+        const bool whole = __all_sync(0xffffffffu, slot >= 0);
+        if (!kList && whole && a.page_size >= kSpan) {
+            // one stretch of one page
+            const int first = __shfl_sync(0xffffffffu, slot, 0);
+            const int in = first & (a.page_size - 1);
+            const int64_t page = (int64_t)(first >> a.ps_shift) * a.page_bytes + head_at;
+            const int64_t from = page + in * kRow + lane * 16;
+            const int64_t sc = page + a.page_size * kRow + (in + lane) * kScales;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const uint32_t to = base + place((i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces * 16);
+                copy_async_all<16>(to, c0 + from + i * 512);
+                if (kCaches == 2) copy_async_all<16>(to + stride, c1 + from + i * 512);
+            }
+            copy_async_all<kScales>(base + scales + lane * kScales, c0 + sc);
+            if (kCaches == 2) copy_async_all<kScales>(base + scales + scale_stride + lane * kScales, c1 + sc);
+        } else {
+            const int at = max(slot, 0);
+            const int64_t page = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at;
+            const int64_t mine = page + (at & (a.page_size - 1)) * kRow;
+            const int64_t sc = page + a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
-                const int at = __shfl_sync(0xffffffffu, slot, t);
-                const int64_t from = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
-                                     (max(at, 0) & (a.page_size - 1)) * kRow + o;
-                copy_async<16>(base + (kTile ? tile_at<D>(t, o) : code_at<D>(t, o)), cache + from, at >= 0);
+                const int64_t from = __shfl_sync(0xffffffffu, mine, t) + o;
+                const bool take = __shfl_sync(0xffffffffu, slot, t) >= 0;
+                const uint32_t to = base + place(t, o);
+                copy_async<16>(to, c0 + from, take);
+                if (kCaches == 2) copy_async<16>(to + stride, c1 + from, take);
             }
-            const int at = max(slot, 0);
-            const int64_t from = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
-                                 a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
-            copy_async<kScales>(base + kSpan * kRow + lane * kScales, cache + from, slot >= 0);
+            copy_async<kScales>(base + scales + lane * kScales, c0 + sc, slot >= 0);
+            if (kCaches == 2) copy_async<kScales>(base + scales + scale_stride + lane * kScales, c1 + sc, slot >= 0);
         }
+    }
+
+    // One cache's span: codes, then scales. One copy group, empty if there is no span.
+    __device__ __forceinline__ void issue_one(const AttentionArgs& a, const uint8_t* cache, uint32_t base) {
+        if (any) copy<1>(a, cache, nullptr, base, 0, kSpan * kRow, 0);
         ptx::cp_async_commit();
         resolve(a);
     }
 
-    // Copies the span into ring slot `base` (number `stage`): K codes, V codes, K
-    // scales, V scales, zeros where there is no token; one copy group, empty if none.
+    // Both caches' (ring slot number `stage`): K codes, V codes, K scales, V scales.
     __device__ __forceinline__ void issue(const AttentionArgs& a, uint32_t base, int stage) {
         if (any) {
-            constexpr int kPieces = kRow / 16;  // 16-byte pieces of a token's codes
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
-                const int at = __shfl_sync(0xffffffffu, slot, t);
-                const int64_t from = (int64_t)(max(at, 0) >> a.ps_shift) * a.page_bytes + head_at +
-                                     (max(at, 0) & (a.page_size - 1)) * kRow + o;
-                const uint32_t to = kTile ? tile_at<D>(t, o) : code_at<D>(t, o);
-                copy_async<16>(base + to, a.k + from, at >= 0);
-                copy_async<16>(base + kSpan * kRow + to, a.v + from, at >= 0);
-            }
-            const int at = max(slot, 0);
-            const int64_t from = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at +
-                                 a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
-            const uint32_t sc = base + 2 * kSpan * kRow + lane * kScales;
-            copy_async<kScales>(sc, a.k + from, slot >= 0);
-            copy_async<kScales>(sc + kSpan * kScales, a.v + from, slot >= 0);
+            copy<2>(a, a.k, a.v, base, kSpan * kRow, 2 * kSpan * kRow, kSpan * kScales);
             if constexpr (kList) {
                 const uint32_t m = __ballot_sync(0xffffffffu, slot >= 0);
                 if (lane == stage) seen = m;

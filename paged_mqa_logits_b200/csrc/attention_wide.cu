@@ -175,21 +175,21 @@ __device__ __forceinline__ void dequant_row(uint32_t codes, uint32_t scales, uin
     } else {
         sc[0] = lds32(scales + lane * 4);
     }
-    const uint32_t line = tile + row * 128;
-#pragma unroll 1
+    const uint32_t line = (tile + row * 128) | ((row & 7) << 4);  // a 16-byte unit's place: its number, xor row % 8
+    const uint32_t from = codes + tile_at<D>(lane, 0);
+#pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-        const uint4 v = lds128(codes + tile_at<D>(lane, j * 16));
+        const uint4 v = lds128(from ^ (j * 16));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t h = e4m3x2_to_f16((D == 128 && j > 1 ? sc[D / 64 - 1] : sc[0]) >> ((j & 1) * 16));
+        const uint32_t h = e4m3x2_to_f16(sc[j / 2] >> ((j & 1) * 16));
         const uint32_t s[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t f[4];
             e2m1_to_f16(w[i], f);
-            const int u = 4 * j + i;  // 16-byte unit of the row
-            sts128(line + (u >> 3) * (kTokens * 128) + (((u & 7) ^ (row & 7)) << 4),
-                   mul_f16x2(f[0], s[i / 2]), mul_f16x2(f[1], s[i / 2]), mul_f16x2(f[2], s[i / 2]),
-                   mul_f16x2(f[3], s[i / 2]));
+            const int u = 4 * j + i;
+            sts128((line ^ ((u & 7) << 4)) + (u >> 3) * (kTokens * 128), mul_f16x2(f[0], s[i / 2]),
+                   mul_f16x2(f[1], s[i / 2]), mul_f16x2(f[2], s[i / 2]), mul_f16x2(f[3], s[i / 2]));
         }
     }
 }
