@@ -22,7 +22,7 @@ namespace {
 // NT: query rows of a CTA / 8. More rows take more registers, so fewer warps.
 template <int D, int NT>
 struct Shape {
-    static constexpr int kWarps = NT == 1 ? 16 : NT == 2 ? 12 : 8;
+    static constexpr int kWarps = NT == 1 ? 16 : 12;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRow = D / 2;                       // code bytes of a token
     static constexpr int kScales = D / 16;                   // scale bytes of a token
@@ -489,7 +489,6 @@ template <int D, typename T, bool kList>
 cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
     const cudaError_t e = a.rows <= 8    ? launch_narrow<D, 1, T, kList>(device, a, stream, pdl)
                           : a.rows <= 16 ? launch_narrow<D, 2, T, kList>(device, a, stream, pdl)
-                          : a.rows <= 32 ? launch_narrow<D, 4, T, kList>(device, a, stream, pdl)
                                          : launch_wide<D, T, kList>(device, a, stream, pdl);
     if (e != cudaSuccess || (kList && a.splits == 1)) return e;
     const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;

@@ -45,7 +45,7 @@ inline int64_t attention_slots(const AttentionArgs& a) {
     return a.splits > 1 ? (int64_t)a.batch * a.next_n * a.splits : 0;
 }
 
-// attention_wide.cu: the kernel for more than 32 query rows a kv head.
+// attention_wide.cu: the kernel for more than 16 query rows a kv head.
 template <int D, typename T, bool kList>
 cudaError_t launch_wide(int device, const AttentionArgs& a, void* stream, bool pdl);
 

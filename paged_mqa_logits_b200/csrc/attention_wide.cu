@@ -1,11 +1,14 @@
-// Attention over the FP4 cache for many query rows a kv head (33 to 128): both
+// Attention over the FP4 cache for many query rows a kv head (17 to 128): both
 // products on the 5th-generation tensor core.
 //
 // A tile is 128 tokens. S = Q K^T (M = 128 query rows, N = 128 tokens) with Q and K,
 // dequantised to f16, in shared memory; P = 2^(S - m) goes back to TMEM, and
 // O += P V with P as the A operand from TMEM and V in shared memory (tokens are the
 // contraction, so V is the MN-major operand and needs no transpose). Rows are TMEM
-// lanes: a thread has a row, and maxima and sums need no exchange.
+// lanes: a thread has a row, and maxima and sums need no exchange. With 64 rows or
+// fewer (32 or fewer), the rows stand in TMEM twice (four times), and each copy takes
+// its half (quarter) of every tile's tokens, with zeros in the other columns of P:
+// all warps have work, and the copies are summed at the end of the row.
 //
 // Warps: 0 issues S and 1 O; 4-7 and 8-11 softmax (a warp has 32 rows; the two
 // groups take tiles in turn, so that one group's exponentials run while the other's
@@ -45,11 +48,16 @@ struct Wide {
     static constexpr int kSlot = kSpan * (kRow + kScales);
     static constexpr int kStages = 3;
     static constexpr int kBuf = kTokens * D * 2;  // a tile of K or V: [D / 64][128 tokens][64] f16, 128-byte swizzle
-    static constexpr int kK = 0, kV = 2 * kBuf, kQ = 4 * kBuf, kRing = 5 * kBuf;
+    static constexpr int kK = 0, kV = 2 * kBuf, kQ = 4 * kBuf;
+    // [2][128][32] fp32: where copies of rows are summed; for D = 128 in Q's place, which
+    // is free then (and a group's part of it is what the same warps write next)
+    static constexpr int kSum = D == 128 ? kQ : kQ + kBuf;
+    static constexpr int kRing = kSum + 2 * 128 * 32 * 4;
     static constexpr int kExch = kRing + 2 * kDequantWarps * kStages * kSlot;  // [2][2][128] fp32
     static constexpr int kRef = kExch + 2 * 2 * 128 * 4;                       // [128] fp32: m of each row
-    static constexpr int kBars = kRef + 128 * 4;
-    static constexpr int kSmem = kBars + 256 + 1024;  // slack for aligning the base
+    static constexpr int kTot = kRef + 128 * 4;                                // [2][128] fp32: sums of p
+    static constexpr int kBars = kTot + 2 * 128 * 4;
+    static constexpr int kSmem = kBars + 320 + 1024;  // slack for aligning the base
     static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
 };
 
@@ -58,17 +66,21 @@ struct Bars {
     uint64_t s_full[kBufS];         // S computed (and its K buffer free)
     uint64_t p_full[kBufS];         // a group's warps arrive: P written
     uint64_t s_free[kBufS];         // P used
-    uint64_t pv_done[2];            // O updated (and its V buffer free)
+    uint64_t pv_done[2];            // V used
     uint64_t q_full;                // the softmax warps arrive: Q is in shared memory
     uint64_t turn[4][2];            // a row quarter's m is settled for the tile
     uint64_t pair[4];               // the two warps of a row quarter exchange values
+    uint64_t copies[2];             // a group's warps: at the row's end, where rows stand in copies
     uint64_t drain[2];
     int32_t abort;
     uint32_t tmem;
 };
-static_assert(sizeof(Bars) <= 256, "barriers");
+static_assert(sizeof(Bars) <= 320, "barriers");
 
-// Waits for phase `parity`, by one thread. False: give up.
+// Waits for phase `parity`, by one thread. False: give up. A wait tells a phase from
+// the one before it, not from the one before that: who waits must know that the
+// barrier's phase before the awaited one is over. Each wait below has that from an
+// earlier wait of the same warp on the same barrier, or from one that its comment names.
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Bars* bars, const StatusWords& st) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer();
@@ -220,7 +232,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         }
         ptx::mbar_init(&bars->q_full, kSoftmaxWarps);
         for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->pair[q], 2);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&bars->drain[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&bars->copies[i], kSoftmaxWarps / 2);
+            ptx::mbar_init(&bars->drain[i], 1);
+        }
         bars->abort = 0;
         ptx::fence_mbar_init();
     }
@@ -339,18 +354,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     } else if (warp >= kSoftmaxWarp) {
         // ------------------------------------------------------------ softmax
         const int q4 = warp & 3, group = (warp - kSoftmaxWarp) >> 2;
-        const int row = q4 * 32 + lane;
-        const bool active = q4 * 32 < a.rows;  // the quarter has query rows
+        const int blocks = a.rows <= 32 ? 1 : a.rows <= 64 ? 2 : 4;  // of 32 rows; 4 / blocks copies of them
+        const int place = q4 * 32 + lane;                 // of this thread in TMEM
+        const int row = q4 % blocks * 32 + lane;          // its query row,
+        const int copy = q4 / blocks;                     // which copy of it, with columns
+        const int chunk0 = copy * blocks, chunk1 = chunk0 + blocks;  // [32 chunk0, 32 chunk1) of a tile
+        const bool active = row - lane < a.rows;          // the quarter has query rows
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
-        uint32_t swaps = 0;
+        uint32_t swaps = 0, seg = 0, meets = 0;  // exchanges, rows and meetings so far
+        // a meeting of the group's warps
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->copies[group]);
+            return wait_phase(&bars->copies[group], meets++ & 1, bars, a.status, lane);
+        };
         // the other group's value for this row
         auto swap = [&](float mine, float& other) {
             float* at = exch + (swaps & 1) * 256;
-            at[group * 128 + row] = mine;
+            at[group * 128 + place] = mine;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->pair[q4]);
             const bool got = wait_phase(&bars->pair[q4], swaps & 1, bars, a.status, lane);
-            other = at[(group ^ 1) * 128 + row];
+            other = at[(group ^ 1) * 128 + place];
             ++swaps;
             return got;
         };
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const int u = group * (D / 16) + i;  // 16-byte unit of the row
-                            sts128(base + W::kQ + (u >> 3) * (kTokens * 128) + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                            sts128(base + W::kQ + (u >> 3) * (kTokens * 128) + place * 128 + (((u & 7) ^ (place & 7)) << 4),
                                    wds[4 * i], wds[4 * i + 1], wds[4 * i + 2], wds[4 * i + 3]);
                         }
                     }
@@ -467,7 +492,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                         // read by then. A loop of small code: unrolled, the kernel's roles
                         // together no longer fit the instruction cache.
 #pragma unroll 1
-                        for (int i = 3; i >= 0; --i) {
+                        for (int i = chunk1 - 1; i >= chunk0; --i) {
                             float s[32];
                             tmem_read32(s_at + 32 * i, s);
                             if (!all) {
@@ -486,7 +511,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                                 const float to = most[0] > m + kSlack ? floorf(most[0]) : m;
                                 scale_l(ex2(m - to));
 #pragma unroll 1
-                                for (int k = 3; k > i; --k) scale_p(p_at + 16 * k, m - to);
+                                for (int k = chunk1 - 1; k > i; --k) scale_p(p_at + 16 * k, m - to);
                                 m = to;
                             }
                             const uint64_t m2 = ptx::f32x2_pack(-m, -m);
@@ -502,22 +527,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                             }
                             ptx::tmem_st16(p_at + 16 * i, p);
                         }
+                        if (blocks < 4) {  // the other copies' columns
+                            const uint32_t zero[16] = {};
+#pragma unroll 1
+                            for (int i = 0; i < 4; ++i)
+                                if (i < chunk0 || i >= chunk1) ptx::tmem_st16(p_at + 16 * i, zero);
+                        }
                         // ---- the m that O has after the tile before
                         if (it > 0) {
                             ok = wait_phase(&bars->turn[q4][b ^ 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
                             if (!ok) break;
                         }
-                        const float had = j > 0 ? ref[row] : m;
+                        const float had = j > 0 ? ref[place] : m;
                         if (__any_sync(0xffffffffu, had != m)) {
                             const float to = fmaxf(had, m);
                             if (__any_sync(0xffffffffu, m < to)) {  // P is behind
                                 scale_l(ex2(m - to));
                                 
 #pragma unroll 1
-                                for (int k = 0; k < 4; ++k) scale_p(p_at + 16 * k, m - to);
+                                for (int k = chunk0; k < chunk1; ++k) scale_p(p_at + 16 * k, m - to);
                             }
                             if (__any_sync(0xffffffffu, had < to)) {  // O is behind
-                                ok = wait_phase(&bars->pv_done[b ^ 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                                ok = wait_phase(&bars->s_free[(it - 1) % kBufS], (it - 1) / kBufS & 1, bars, a.status, lane);
                                 if (!ok) break;
                                 ptx::tc_fence_after();
                                 const float by = ex2(had - to);
@@ -533,7 +564,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                             }
                             m = to;
                         }
-                        if (j == 0 || had != m) ref[row] = m;
+                        if (j == 0 || had != m) ref[place] = m;
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(&bars->turn[q4][b]);
                         ptx::tmem_st_wait();
@@ -544,16 +575,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 }
                 if (!ok) break;
                 // ---- the row's result: each group has half of its columns
-                if (n > 0) {
-                    ok = wait_phase(&bars->pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                if (!active) {
+                    // nothing of it; but the next row is not begun before all have begun this one
+                    ok = n == 0 || wait_phase(&bars->q_full, seg & 1, bars, a.status, lane);
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                }
-                if (active) {
+                } else {
                     if (n > 0) {
-                        ok = wait_phase(&bars->turn[q4][(it - 1) & 1], ((it - 1) >> 1) & 1, bars, a.status, lane);
+                        // the last tile's turn comes first: with it, its S buffer's use before
+                        // that is known to be over, and the wait cannot take that for this one
+                        ok = wait_phase(&bars->turn[q4][(it - 1) & 1], ((it - 1) >> 1) & 1, bars, a.status, lane) &&
+                             wait_phase(&bars->s_free[(it - 1) % kBufS], (it - 1) / kBufS & 1, bars, a.status, lane);
                         if (!ok) break;
-                        const float to = ref[row];  // settled by the last tile
+                        ptx::tc_fence_after();
+                        const float to = ref[place];
                         float l0, l1;
                         ptx::f32x2_unpack(l2, l0, l1);
                         l = (l0 + l1) * ex2(m - to);
@@ -563,37 +597,82 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     ok = swap(l, other);
                     if (!ok) break;
                     l = group ? other + l : l + other;
+                    float by = 1.f;  // what this copy's O is multiplied by
+                    if (n > 0 && blocks < 4) {
+                        float* tot = reinterpret_cast<float*>(smem + W::kTot) + group * 128;
+                        tot[place] = l;
+                        ok = meet();
+                        if (!ok) break;
+                        float top = kUnset;
+                        for (int k = row; k < 128; k += 32 * blocks) top = fmaxf(top, ref[k]);
+                        l = 0.f;
+                        for (int k = row; k < 128; k += 32 * blocks) l += tot[k] * ex2(ref[k] - top);
+                        by = ex2(m - top);
+                        m = top;
+                    }
                     int64_t slot;
                     const bool whole = row_is_whole<kList>(a, r, slot);
                     const int64_t at_part = (slot * a.kv_heads + r.hk) * a.rows + row;
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        float o[16];
-                        const int d = group * (D / 2) + 16 * i;
-                        if (n > 0) {
-                            tmem_read16(lanes + kColO + d, o);
+                    // 8 elements of the row's result, from element d on
+                    auto put = [&](int d, const float* o) {
+                        if (row >= a.rows) return;
+                        if (whole) {
+                            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at_row * D + d) =
+                                make_uint4(pack<T>(o[0] * inv, o[1] * inv), pack<T>(o[2] * inv, o[3] * inv),
+                                           pack<T>(o[4] * inv, o[5] * inv), pack<T>(o[6] * inv, o[7] * inv));
                         } else {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+                            float4* out = reinterpret_cast<float4*>(a.part_o + at_part * D + d);
+                            out[0] = make_float4(o[0], o[1], o[2], o[3]);
+                            out[1] = make_float4(o[4], o[5], o[6], o[7]);
                         }
-                        if (row < a.rows) {
-                            if (whole) {
-                                uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at_row * D + d);
-                                uint32_t v[8];
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) v[k] = pack<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
-                                out[0] = make_uint4(v[0], v[1], v[2], v[3]);
-                                out[1] = make_uint4(v[4], v[5], v[6], v[7]);
-                            } else {
-                                float4* out = reinterpret_cast<float4*>(a.part_o + at_part * D + d);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    out[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    };
+                    if (n == 0 || blocks == 4) {
+#pragma unroll 1
+                        for (int i = 0; i < D / 32; ++i) {
+                            float o[16] = {};
+                            const int d = group * (D / 2) + 16 * i;
+                            if (n > 0) tmem_read16(lanes + kColO + d, o);
+                            if (copy == 0) {
+                                put(d, o);
+                                put(d + 8, o + 8);
                             }
                         }
+                    } else {
+                        // 32 columns at a time: every copy leaves its own, then a warp sums
+                        // 32 / (4 / blocks) of them over the copies
+                        const uint32_t sums = base + W::kSum + group * (128 * 32 * 4);
+#pragma unroll 1
+                        for (int i = 0; i < D / 64; ++i) {
+                            const int d = group * (D / 2) + 32 * i;
+                            float o[32];
+                            tmem_read32(lanes + kColO + d, o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                sts128(sums + place * 128 + ((k ^ (place & 7)) << 4), __float_as_uint(o[4 * k] * by),
+                                       __float_as_uint(o[4 * k + 1] * by), __float_as_uint(o[4 * k + 2] * by),
+                                       __float_as_uint(o[4 * k + 3] * by));
+                            ok = meet();
+                            if (!ok) break;
+#pragma unroll 1
+                            for (int e = 8 * blocks * copy; e < 8 * blocks * (copy + 1); e += 8) {
+                                float v[8] = {};
+                                for (int k = row; k < 128; k += 32 * blocks) {
+                                    const uint4 x = lds128(sums + k * 128 + (((e >> 2) ^ (k & 7)) << 4));
+                                    const uint4 y = lds128(sums + k * 128 + (((e >> 2) + 1 ^ (k & 7)) << 4));
+                                    v[0] += __uint_as_float(x.x); v[1] += __uint_as_float(x.y);
+                                    v[2] += __uint_as_float(x.z); v[3] += __uint_as_float(x.w);
+                                    v[4] += __uint_as_float(y.x); v[5] += __uint_as_float(y.y);
+                                    v[6] += __uint_as_float(y.z); v[7] += __uint_as_float(y.w);
+                                }
+                                put(d + e, v);
+                            }
+                            ok = meet();
+                            if (!ok) break;
+                        }
+                        if (!ok) break;
                     }
-                    if (row < a.rows && group == 0) {
+                    if (row < a.rows && group == 0 && copy == 0) {
                         if (whole) {
                             if (a.lse != nullptr) a.lse[at_row] = lse_of(m, l);
                         } else {
@@ -602,6 +681,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     }
                 }
                 ptx::tc_fence_before();
+                seg += n > 0;
                 next_row<kList>(a, r);
             }
         } while (ok && pair < pairs_end && !kList);

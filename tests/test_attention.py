@@ -109,6 +109,12 @@ DENSE = [
     ([1100, 3], 2, 33, 1, 64, 32, "f16", 4),
     ([520, 100, 256], 1, 65, 1, 64, 256, "bf16", 2),
     ([3000, 1], 4, 32, 1, 128, 64, "bf16", 6),
+    # 17 to 128 rows a kv head, several heads and rows to a CTA, odd and even numbers of tiles
+    ([333, 90, 128, 0, 1], 1, 51, 3, 128, 16, "f16", 1),
+    ([128, 256, 129], 3, 44, 4, 64, 32, "bf16", 2),
+    ([70, 513, 700], 2, 192, 3, 128, 64, "bf16", 4),
+    ([1200, 5], 1, 80, 1, 128, 64, "f16", 3),
+    ([300, 900, 77], 4, 40, 5, 64, 64, "bf16", 7),
 ]
 
 
@@ -128,6 +134,8 @@ LISTS = [
     ([40], 1, 1, 1, 64, 16, "bf16", 1),
     ([1200, 5], 1, 64, 1, 128, 64, "bf16", 300),
     ([800, 5], 1, 96, 2, 64, 256, "bf16", 200),
+    ([700, 90, 0], 2, 60, 3, 128, 16, "f16", 300),
+    ([400, 33], 1, 256, 2, 64, 64, "bf16", 129),
 ]
 
 
