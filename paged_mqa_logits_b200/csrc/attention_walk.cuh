@@ -269,8 +269,13 @@ struct SpanLoader {
     const int32_t* list;
     int64_t head_at;
     int lane, off, pos;
-    int slot;       // this lane's token's cache slot (page * page_size + slot), -1 for none,
-    bool any;       // of the span to be copied next, if there is one: found a step ahead
+    // This lane's token of the span to be copied next, found a step ahead: its token
+    // (-1 for none), its page as loaded (not looked at before the copy, so that nothing
+    // waits for the load), and if there is a span at all.
+    int tok, page;
+    bool any;
+    int ahead;      // selected: the list's entry for the span after that, as loaded
+    int slot;       // in copy(): the token's cache slot (page * page_size + slot), -1 for none
     uint32_t seen;  // selected: lane s keeps the mask of the visible tokens in ring slot s
 
     __device__ __forceinline__ void open(const AttentionArgs& a, const Range& range, int lane_, int off_) {
@@ -281,33 +286,28 @@ struct SpanLoader {
         list = kList ? a.indices + (int64_t)r.w.item * a.topk : nullptr;
         head_at = (int64_t)r.hk * a.page_size * (kRow + kScales);
         seen = 0;
+        if constexpr (kList) ahead = pos + lane < r.w.t1 ? __ldg(list + pos + lane) : -1;
         resolve(a);
     }
 
     __device__ __forceinline__ void resolve(const AttentionArgs& a) {
         any = false;
-        slot = -1;
+        tok = -1;
         while (r.more && (kTile ? pos - off : pos) >= r.w.t1) {
             next_row<kList>(a, r);
             pos = r.w.t0 + off;
         }
         if (!r.more) return;
         any = true;
-        int t = pos + lane;
+        const int t = pos + lane;
         pos += kStep;
-        bool ok = t < r.w.t1;
         if constexpr (kList) {
-            t = ok ? __ldg(list + t) : -1;
-            ok = t >= 0 && t < r.w.ctx;
+            tok = ahead >= 0 && ahead < r.w.ctx ? ahead : -1;
+            ahead = pos + lane < r.w.t1 ? __ldg(list + pos + lane) : -1;
+        } else {
+            tok = t < r.w.t1 ? t : -1;
         }
-        if (ok) {
-            int page = __ldg(a.block_table + (int64_t)r.w.b * a.max_pages + (t >> a.ps_shift));
-            if (page < 0 || page >= a.num_pages) {
-                report_checked(a.status, MQA_STATUS_BAD_PAGE);
-                page = page < 0 ? 0 : a.num_pages - 1;
-            }
-            slot = (page << a.ps_shift) | (t & (a.page_size - 1));
-        }
+        page = __ldg(a.block_table + (int64_t)r.w.b * a.max_pages + (max(tok, 0) >> a.ps_shift));
     }
 
     // Copies the span's codes and scales of `caches` caches (K, then V, to slots
@@ -318,6 +318,11 @@ struct SpanLoader {
                                          uint32_t stride, uint32_t scales, uint32_t scale_stride) {
         constexpr int kPieces = kRow / 16;  // 16-byte pieces of a token's codes
         auto place = [](int t, int o) { return kTile ? tile_at<D>(t, o) : code_at<D>(t, o); };
+        if (page < 0 || page >= a.num_pages) {
+            if (tok >= 0) report_checked(a.status, MQA_STATUS_BAD_PAGE);
+            page = page < 0 ? 0 : a.num_pages - 1;
+        }
+        slot = tok >= 0 ? (page << a.ps_shift) | (tok & (a.page_size - 1)) : -1;
         const bool whole = __all_sync(0xffffffffu, slot >= 0);
         if (!kList && whole && a.page_size >= kSpan) {
             // one stretch of one page
