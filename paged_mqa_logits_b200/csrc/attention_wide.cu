@@ -15,8 +15,8 @@
 // products do), 12-15 dequantise K and 16-19 V (32 tokens of each tile, through rings
 // of asynchronous copies of their own). S, K and V have two buffers each.
 //
-// m is raised, by whole numbers so that every rescaling is exact, only when a score
-// exceeds it by kSlack (see attention.cu). A tile is computed with the m that its
+// m is raised, by whole numbers so that every rescaling is exact, only when the p of
+// 32 tokens sum to more than kMost (so that none is outside f16). A tile is computed with the m that its
 // group knows; at its end the group learns the m that O has by then (`ref`, settled
 // in turn, tile by tile) and scales whichever of P and O is behind, which is rare. So
 // a tile needs one pass over S, and the groups wait for each other only where one
@@ -36,6 +36,7 @@ constexpr int kDequantWarps = 4;   // for each of K and V
 // in their quarters of TMEM), then the softmax and the dequantising warps.
 constexpr int kMmaWarp = 0, kSoftmaxWarp = 4, kDequantWarp = kSoftmaxWarp + kSoftmaxWarps;
 constexpr int kWideThreads = 32 * (kDequantWarp + 2 * kDequantWarps);
+constexpr float kMost = 32768.f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 // TMEM columns: three S buffers of 128 (P over their second halves), O. With three, S
 // is two tiles ahead and no group waits for a product; Q is in shared memory for it.
@@ -435,6 +436,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     if (lane == 0) ptx::mbar_arrive(&bars->q_full);
                 }
                 fac = fmaxf(fac, 1e-37f);  // a factor of 0 must not make NaN of an invisible column's -inf
+                const int it0 = it;
                 const uint64_t fac2 = ptx::f32x2_pack(fac, fac);
                 uint64_t l2 = 0;  // two partial sums of p, relative to m
                 auto scale_l = [&](float by) {
@@ -453,8 +455,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     for (int k = 0; k < 16; ++k) v[k] = mul_f16x2(mul_f16x2(__float_as_uint(p[k]), by0), by1);
                     ptx::tmem_st16(at, v);
                 };
-                for (int j = 0; j < n; ++j, ++it) {
-                    if ((it & 1) != group) continue;
+                for (int j = (it & 1) ^ group; j < n; j += 2) {
+                    const int it = it0 + j;
                     const uint32_t b = group, sb = it % kBufS;
                     const uint32_t s_at = lanes + sb * 128, p_at = s_at + kColP;
                     const int t = w.t0 + j * kTokens;
@@ -494,37 +496,54 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
 #pragma unroll 1
                         for (int i = chunk1 - 1; i >= chunk0; --i) {
                             float s[32];
-                            tmem_read32(s_at + 32 * i, s);
-                            if (!all) {
-                                const uint32_t see = i == 0 ? see0 : i == 1 ? see1 : i == 2 ? see2 : see3;
+                            uint32_t p[16];
+                            uint64_t sum;
+                            auto read = [&]() {
+                                tmem_read32(s_at + 32 * i, s);
+                                if (!all) {
+                                    const uint32_t see = i == 0 ? see0 : i == 1 ? see1 : i == 2 ? see2 : see3;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
-                            }
-                            float most[2] = {s[0], s[1]};
+                                    for (int k = 0; k < 32; ++k) s[k] = (see >> k) & 1 ? s[k] : -INFINITY;
+                                }
+                            };
+                            auto powers = [&]() {
+                                const uint64_t m2 = ptx::f32x2_pack(-m, -m);
+                                uint64_t sums[2];
 #pragma unroll
-                            for (int k = 2; k < 30; k += 4) {
-                                most[0] = max3(most[0], s[k], s[k + 1]);
-                                most[1] = max3(most[1], s[k + 2], s[k + 3]);
-                            }
-                            most[0] = max3(max3(most[0], s[30], s[31]), most[1], most[1]) * fac;
-                            if (__any_sync(0xffffffffu, most[0] > m + kSlack)) {
-                                const float to = most[0] > m + kSlack ? floorf(most[0]) : m;
+                                for (int k = 0; k < 16; ++k) {
+                                    float e0, e1;
+                                    ptx::f32x2_unpack(ptx::fma_f32x2(ptx::f32x2_pack(s[2 * k], s[2 * k + 1]), fac2, m2), e0, e1);
+                                    e0 = ex2(e0);
+                                    e1 = ex2(e1);
+                                    const uint64_t e2 = ptx::f32x2_pack(e0, e1);
+                                    sums[k & 1] = k < 2 ? e2 : add_f32x2(sums[k & 1], e2);
+                                    p[k] = pack_f16(e0, e1);
+                                }
+                                sum = add_f32x2(sums[0], sums[1]);
+                            };
+                            read();
+                            powers();
+                            // no p is above the sums: within f16, or m has to rise
+                            float sum0, sum1;
+                            ptx::f32x2_unpack(sum, sum0, sum1);
+                            if (__any_sync(0xffffffffu, sum0 + sum1 > kMost)) {
+                                read();
+                                float most[2] = {s[0], s[1]};
+#pragma unroll
+                                for (int k = 2; k < 30; k += 4) {
+                                    most[0] = max3(most[0], s[k], s[k + 1]);
+                                    most[1] = max3(most[1], s[k + 2], s[k + 3]);
+                                }
+                                // every row of the warp goes along, to what it sees here: the
+                                // rescaling costs the warp the same, and the next one comes later
+                                const float to = fmaxf(m, floorf(max3(max3(most[0], s[30], s[31]), most[1], most[1]) * fac));
                                 scale_l(ex2(m - to));
 #pragma unroll 1
                                 for (int k = chunk1 - 1; k > i; --k) scale_p(p_at + 16 * k, m - to);
                                 m = to;
+                                powers();
                             }
-                            const uint64_t m2 = ptx::f32x2_pack(-m, -m);
-                            uint32_t p[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                float e0, e1;
-                                ptx::f32x2_unpack(ptx::fma_f32x2(ptx::f32x2_pack(s[2 * k], s[2 * k + 1]), fac2, m2), e0, e1);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                                l2 = add_f32x2(l2, ptx::f32x2_pack(e0, e1));
-                                p[k] = pack_f16(e0, e1);
-                            }
+                            l2 = add_f32x2(l2, sum);
                             ptx::tmem_st16(p_at + 16 * i, p);
                         }
                         if (blocks < 4) {  // the other copies' columns
@@ -573,6 +592,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&bars->p_full[sb]);
                 }
+                it = it0 + n;
                 if (!ok) break;
                 // ---- the row's result: each group has half of its columns
                 if (!active) {
