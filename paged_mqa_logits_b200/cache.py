@@ -12,12 +12,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import struct
 from typing import Optional, Sequence, Union
 
 import torch
 
 _I32, _I64, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_INT, _BYTE, _FLOAT = torch.int32, torch.uint8, torch.float32
 MQA_PAGES_MAX_CACHES = 256
 
 
@@ -47,27 +49,40 @@ class PagesParams(ctypes.Structure):
         ("flags", ctypes.c_uint32), ("status", _P)]
 
 
+# The calls below pack the same structs into bytes: a fifth of the time that filling
+# a ctypes.Structure takes, and small calls are bound by the host.
+_ATTENTION, _APPEND, _PAGES = struct.Struct("@11iIfi3qQP"), struct.Struct("@8iIi4qP"), struct.Struct("@5iIP")
+assert _ATTENTION.size == ctypes.sizeof(AttentionParams)
+assert _APPEND.size == ctypes.sizeof(AppendParams)
+assert _PAGES.size == ctypes.sizeof(PagesParams)
+
+
 def declare(lib) -> None:
     """Argument types of the entry points of include/mqa_cache.h."""
-    a, n, p = (ctypes.POINTER(t) for t in (AttentionParams, AppendParams, PagesParams))
     for name, types in {
-        "paged_mqa_attention_fp4": [_P] * 10 + [a, _P],
-        "mqa_attention_workspace_size": [a, ctypes.POINTER(ctypes.c_uint64)],
-        "mqa_cache_append_fp8": [_P] * 6 + [n, _P],
-        "mqa_cache_append_fp4": [_P] * 9 + [n, _P],
-        "mqa_pages_fork": [_P] * 6 + [p, _P],
-        "mqa_pages_resize": [_P] * 6 + [p, _P],
-        "mqa_pages_compact": [_P] * 7 + [p, _P],
-        "mqa_pages_copy": [_P, _P, _I32, _P, _P, _I32, _P, p, _P],
+        "paged_mqa_attention_fp4": [_P] * 12,
+        "mqa_attention_workspace_size": [_P, _P],
+        "mqa_cache_append_fp8": [_P] * 8,
+        "mqa_cache_append_fp4": [_P] * 11,
+        "mqa_pages_fork": [_P] * 8,
+        "mqa_pages_resize": [_P] * 8,
+        "mqa_pages_compact": [_P] * 9,
+        "mqa_pages_copy": [_P, _P, _I32, _P, _P, _I32, _P, _P, _P],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = types
         fn.restype = ctypes.c_int
 
 
+_library = None
+
+
 def _lib():
-    from . import library
-    return library()
+    global _library
+    if _library is None:
+        from . import library
+        _library = library()
+    return _library
 
 
 def _check(rc: int) -> None:
@@ -76,57 +91,58 @@ def _check(rc: int) -> None:
         check(rc)
 
 
-class _Call:
-    """Device and stream of one call: entered around the allocations and the launch."""
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t's device and `stream` needs the current ones changed."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return stream is not None or dev != torch.cuda.current_device()
 
-    __slots__ = ("device", "stream", "_guards")
 
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors must be CUDA tensors")
-        self.device, self._guards = device, None
-        guards = []
-        if device.index != torch.cuda.current_device():
-            guards.append(torch.cuda.device(device))
+@contextlib.contextmanager
+def _there(t: torch.Tensor, stream):
+    """t's device and `stream` (None: the device's current one) as the current ones."""
+    with torch.cuda.device(t.device):
         if stream is None:
-            self.stream = torch.cuda.current_stream(device).cuda_stream
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.stream = stream.cuda_stream
-            guards.append(torch.cuda.stream(stream))
-        if guards:
-            self._guards = contextlib.ExitStack()
-            for g in guards:
-                self._guards.enter_context(g)
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.stream(stream):
+            yield
 
-    def __enter__(self):
-        return self
 
-    def __exit__(self, *exc):
-        if self._guards is not None:
-            self._guards.close()
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def ptr(self, t: Optional[torch.Tensor], name: str, dtype, shape=None, numel=None):
-        """Device pointer of a contiguous tensor (None: NULL) after its checks."""
-        if t is None:
-            return None
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if t.dtype != dtype:
+
+def _ptr(t: Optional[torch.Tensor], dev: int, dtype, name: str):
+    """Device pointer of a contiguous tensor (None: NULL) after its checks."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected CUDA device {dev}")
+        if t.dtype is not dtype:
             raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{name} must hold {numel} entries (got {t.numel()})")
-        return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+
+def _shaped(t: Optional[torch.Tensor], shape, dev: int, dtype, name: str):
+    """The same of a tensor with a given shape."""
+    if t is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    return _ptr(t, dev, dtype, name)
+
+
+def _sized(t: Optional[torch.Tensor], n: int, dev: int, dtype, name: str):
+    """The same of a tensor with n entries."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} entries (got {t.numel()})")
+    return _ptr(t, dev, dtype, name)
 
 
 def _page_size(cache: torch.Tensor, row_bytes: int, page_size: Optional[int], name: str) -> int:
@@ -142,12 +158,18 @@ def _page_size(cache: torch.Tensor, row_bytes: int, page_size: Optional[int], na
     return page_size
 
 
-def _table(call: _Call, block_table, context_lens, batch):
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table must be [{batch}, max_pages_per_row] "
-                         f"(got {list(block_table.shape)})")
-    return (call.ptr(block_table, "block_table", torch.int32),
-            call.ptr(context_lens, "context_lens", torch.int32, numel=batch))
+def _width(block_table: torch.Tensor, batch: int) -> int:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, max_pages_per_row] (got {list(shape)})")
+    return shape[1]
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16 or float16")
+    return code
 
 
 # ---------------------------------------------------------------- attention
@@ -158,21 +180,21 @@ def mqa_attention_workspace(q: torch.Tensor, *, kv_heads: int = 1, topk: int = 0
     topk. One serves every layer and step, but not two calls at the same time."""
     if q.dim() != 4:
         raise ValueError("q must be [B, next_n, H, D]")
+    if _elsewhere(q, None):
+        with _there(q, None):
+            return mqa_attention_workspace(q, kv_heads=kv_heads, topk=topk, num_ctas=num_ctas)
     if num_ctas is None:
         num_ctas = torch.cuda.get_device_properties(q.device).multi_processor_count
     B, next_n, H, D = q.shape
-    with _Call(q.device, None) as call:
-        p = AttentionParams(B, next_n, H, kv_heads, D, 64, 1, 1, topk, num_ctas,
-                            _dtype(q, "q"), 0, 1.0, 0)
-        size = ctypes.c_uint64(0)
-        _check(_lib().mqa_attention_workspace_size(ctypes.byref(p), ctypes.byref(size)))
-        return call.empty(size.value, torch.uint8)
+    p = _ATTENTION.pack(B, next_n, H, kv_heads, D, 64, 1, 1, topk, num_ctas, _dtype(q, "q"), 0,
+                        1.0, 0, 0, 0, 0, 0, 0)
+    return torch.empty(_workspace_bytes(p), dtype=_BYTE, device=q.device)
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16 or float16")
-    return _DTYPES[t.dtype]
+def _workspace_bytes(params: bytes) -> int:
+    size = ctypes.c_uint64(0)
+    _check(_lib().mqa_attention_workspace_size(params, ctypes.byref(size)))
+    return size.value
 
 
 def paged_mqa_attention_fp4(q, k_cache, v_cache, block_table, context_lens, schedule=None, *,
@@ -197,72 +219,62 @@ def paged_mqa_attention_fp4(q, k_cache, v_cache, block_table, context_lens, sche
         raise ValueError("q must be [B, next_n, H, D]")
     if (schedule is None) == (indices is None):
         raise ValueError("give either schedule or indices")
-    B, next_n, H, D = q.shape
-    if q.stride(3) != 1:
+    B, next_n, H, D = shape = q.shape
+    sb, sn, sh, sd = q.stride()
+    if sd != 1:
         raise ValueError("the last dimension of q must be contiguous")
     dtype = _dtype(q, "q")
     if k_cache.shape != v_cache.shape:
         raise ValueError(f"k_cache and v_cache differ in shape ({list(k_cache.shape)}, "
                          f"{list(v_cache.shape)})")
     page_size = _page_size(k_cache, kv_heads * (D // 2 + D // 16), page_size, "k_cache")
-    topk, num_ctas = 0, 0
-    if indices is not None:
-        if indices.dim() != 3 or indices.shape[0] != B or indices.shape[1] != next_n:
+    width = _width(block_table, B)
+    if indices is None:
+        topk, num_ctas = 0, schedule.numel() // 2 - 1
+    else:
+        topk, num_ctas = indices.shape[-1], 0
+        if indices.shape != (B, next_n, topk):
             raise ValueError(f"indices must be [{B}, {next_n}, k] (got {list(indices.shape)})")
-        topk = indices.shape[2]
         if topk < 1:
             raise ValueError("indices must list at least one entry a position")
-    else:
-        num_ctas = schedule.numel() // 2 - 1
-    with _Call(q.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        sched = call.ptr(schedule, "schedule", torch.int32)
-        idx = call.ptr(indices, "indices", torch.int32)
-        kp = call.ptr(k_cache, "k_cache", torch.uint8)
-        vp = call.ptr(v_cache, "v_cache", torch.uint8)
-        st = call.ptr(status, "status", torch.int32)
-        if out is None:
-            out = call.empty((B, next_n, H, D), q.dtype)
-        op = call.ptr(out, "out", q.dtype, shape=q.shape)
-        if lse is None and with_lse:
-            lse = call.empty((B, next_n, H), torch.float32)
-        lp = call.ptr(lse, "lse", torch.float32, shape=q.shape[:3])
-        p = AttentionParams(B, next_n, H, kv_heads, D, page_size, k_cache.shape[0],
-                            block_table.shape[1], topk, num_ctas, dtype, flags,
-                            D ** -0.5 if scale is None else scale, 0, q.stride(0), q.stride(1),
-                            q.stride(2), 0, st)
-        lib = _lib()
-        if workspace is None:
-            size = ctypes.c_uint64(0)
-            _check(lib.mqa_attention_workspace_size(ctypes.byref(p), ctypes.byref(size)))
-            workspace = call.empty(size.value, torch.uint8)
-        p.workspace_bytes = workspace.numel()
-        wp = call.ptr(workspace, "workspace", torch.uint8)
-        _check(lib.paged_mqa_attention_fp4(q.data_ptr(), kp, vp, table, lens, sched, idx, op, lp,
-                                           wp, ctypes.byref(p), call.stream))
+    if _elsewhere(q, stream):
+        with _there(q, stream):
+            return paged_mqa_attention_fp4(
+                q, k_cache, v_cache, block_table, context_lens, schedule, kv_heads=kv_heads,
+                scale=scale, indices=indices, page_size=page_size, out=out, lse=lse,
+                with_lse=with_lse, workspace=workspace, flags=flags, status=status)
+    dev = q.get_device()
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None and with_lse:
+        lse = torch.empty(shape[:3], dtype=_FLOAT, device=q.device)
+    st = _ptr(status, dev, _INT, "status") or 0
+    if scale is None:
+        scale = D ** -0.5
+
+    def params(size):
+        return _ATTENTION.pack(B, next_n, H, kv_heads, D, page_size, k_cache.shape[0], width, topk,
+                               num_ctas, dtype, flags, scale, 0, sb, sn, sh, size, st)
+
+    if workspace is None:
+        workspace = torch.empty(_workspace_bytes(params(0)), dtype=_BYTE, device=q.device)
+    _check(_lib().paged_mqa_attention_fp4(
+        q.data_ptr(), _ptr(k_cache, dev, _BYTE, "k_cache"), _ptr(v_cache, dev, _BYTE, "v_cache"),
+        _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"), _ptr(schedule, dev, _INT, "schedule"),
+        _ptr(indices, dev, _INT, "indices"), _shaped(out, shape, dev, q.dtype, "out"),
+        None if lse is None else _shaped(lse, shape[:3], dev, _FLOAT, "lse"),
+        _ptr(workspace, dev, _BYTE, "workspace"), params(workspace.numel()), _stream(dev)))
     return out if lse is None else (out, lse)
 
 
 # ---------------------------------------------------------------- appends
-def _tokens(call: _Call, x, name: str, heads: Optional[int]):
-    """Pointer and strides of new tokens [T, D] (heads None) or [T, heads, D]."""
-    if x.device != call.device:
-        raise ValueError(f"{name} is on {x.device}, expected {call.device}")
-    if x.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return x.data_ptr(), x.stride(0), 0 if heads is None else x.stride(1)
-
-
-def _values(call: _Call, values, x, name: str, wanted: bool):
-    if values is None and wanted:
-        values = call.empty(x.shape, x.dtype)
-    return values, call.ptr(values, name, x.dtype, shape=x.shape)
-
-
-def _rows(call: _Call, row_offsets, batch: int):
-    if row_offsets is None:
-        return None
-    return call.ptr(row_offsets, "row_offsets", torch.int32, numel=batch + 1)
+def _values(values, x, dev: int, name: str, wanted: bool):
+    if values is None:
+        if not wanted:
+            return None, None
+        values = torch.empty_like(x, memory_format=torch.contiguous_format)
+    return values, _shaped(values, x.shape, dev, x.dtype, name)
 
 
 def mqa_cache_append_fp8(x, kv_cache, block_table, context_lens, row_offsets=None, *,
@@ -278,18 +290,27 @@ def mqa_cache_append_fp8(x, kv_cache, block_table, context_lens, row_offsets=Non
     if x.dim() != 2:
         raise ValueError("x must be [T, D]")
     T, D = x.shape
+    sx, sd = x.stride()
+    if sd != 1:
+        raise ValueError("the last dimension of x must be contiguous")
     dtype = _dtype(x, "x")
     B = block_table.shape[0]
     page_size = _page_size(kv_cache, D + 4, page_size, "kv_cache")
-    with _Call(x.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        xp, st, _ = _tokens(call, x, "x", None)
-        values, vp = _values(call, values, x, "values", with_values)
-        p = AppendParams(B, T, 1, D, page_size, kv_cache.shape[0], block_table.shape[1], dtype,
-                         flags, 0, st, 0, 0, 0, call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_cache_append_fp8(
-            xp, call.ptr(kv_cache, "kv_cache", torch.uint8), table, lens,
-            _rows(call, row_offsets, B), vp, ctypes.byref(p), call.stream))
+    width = _width(block_table, B)
+    if _elsewhere(x, stream):
+        with _there(x, stream):
+            return mqa_cache_append_fp8(
+                x, kv_cache, block_table, context_lens, row_offsets, page_size=page_size,
+                values=values, with_values=with_values, flags=flags, status=status)
+    dev = x.get_device()
+    values, vp = _values(values, x, dev, "values", with_values)
+    _check(_lib().mqa_cache_append_fp8(
+        x.data_ptr(), _ptr(kv_cache, dev, _BYTE, "kv_cache"),
+        _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"),
+        _sized(row_offsets, B + 1, dev, _INT, "row_offsets"), vp,
+        _APPEND.pack(B, T, 1, D, page_size, kv_cache.shape[0], width, dtype, flags, 0, sx, 0, 0, 0,
+                     _ptr(status, dev, _INT, "status") or 0), _stream(dev)))
     return values
 
 
@@ -301,37 +322,53 @@ def mqa_cache_append_fp4(k, v, k_cache, v_cache, block_table, context_lens, row_
     """Quantise new tokens k and v (bf16 or f16 [T, kv_heads, D]) into FP4 caches
     (uint8 [num_pages, kv_heads * page_size * (D/2 + D/16)]); v and v_cache may be
     None (keys alone, as paged_mqa_logits_fp4 reads them). Rows and positions as
-    for mqa_cache_append_fp8. With with_values returns (k_values, v_values), what
-    the caches now hold for the tokens, in their type."""
+    for mqa_cache_append_fp8. With with_values (or k_values, v_values) returns
+    (k_values, v_values), what the caches now hold for the tokens, in their type."""
     if k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, D]")
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
     T, heads, D = k.shape
+    kt, kh, sd = k.stride()
+    vt = vh = 0
     dtype = _dtype(k, "k")
-    if v is not None and (v.shape != k.shape or v.dtype != k.dtype):
-        raise ValueError("v must have the shape and type of k")
+    if v is not None:
+        if v.shape != k.shape or v.dtype != k.dtype:
+            raise ValueError("v must have the shape and type of k")
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("v_cache must have the shape of k_cache")
+        vt, vh, vd = v.stride()
+        if vd != 1:
+            raise ValueError("the last dimension of v must be contiguous")
+    elif v_values is not None:
+        raise ValueError("v_values without v")
+    if sd != 1:
+        raise ValueError("the last dimension of k must be contiguous")
     B = block_table.shape[0]
     page_size = _page_size(k_cache, heads * (D // 2 + D // 16), page_size, "k_cache")
-    if v_cache is not None and v_cache.shape != k_cache.shape:
-        raise ValueError("v_cache must have the shape of k_cache")
-    if v is None and v_values is not None:
-        raise ValueError("v_values without v")
-    with _Call(k.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        kp, kt, kh = _tokens(call, k, "k", heads)
-        vp, vt, vh = (None, 0, 0) if v is None else _tokens(call, v, "v", heads)
-        k_values, kvp = _values(call, k_values, k, "k_values", with_values)
-        vvp = None
-        if v is not None:
-            v_values, vvp = _values(call, v_values, v, "v_values", with_values)
-        p = AppendParams(B, T, heads, D, page_size, k_cache.shape[0], block_table.shape[1], dtype,
-                         flags, 0, kt, kh, vt, vh, call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_cache_append_fp4(
-            kp, vp, call.ptr(k_cache, "k_cache", torch.uint8),
-            call.ptr(v_cache, "v_cache", torch.uint8), table, lens, _rows(call, row_offsets, B),
-            kvp, vvp, ctypes.byref(p), call.stream))
-    return (k_values, v_values) if with_values or k_values is not None or v_values is not None else None
+    width = _width(block_table, B)
+    if _elsewhere(k, stream):
+        with _there(k, stream):
+            return mqa_cache_append_fp4(
+                k, v, k_cache, v_cache, block_table, context_lens, row_offsets, page_size=page_size,
+                k_values=k_values, v_values=v_values, with_values=with_values, flags=flags,
+                status=status)
+    dev = k.get_device()
+    vp = vvp = None
+    if v is not None:
+        if v.get_device() != dev:
+            raise ValueError(f"v is on {v.device}, expected CUDA device {dev}")
+        vp = v.data_ptr()
+        v_values, vvp = _values(v_values, v, dev, "v_values", with_values)
+    k_values, kvp = _values(k_values, k, dev, "k_values", with_values)
+    _check(_lib().mqa_cache_append_fp4(
+        k.data_ptr(), vp, _ptr(k_cache, dev, _BYTE, "k_cache"),
+        _ptr(v_cache, dev, _BYTE, "v_cache"), _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"),
+        _sized(row_offsets, B + 1, dev, _INT, "row_offsets"), kvp, vvp,
+        _APPEND.pack(B, T, heads, D, page_size, k_cache.shape[0], width, dtype, flags, 0, kt, kh,
+                     vt, vh, _ptr(status, dev, _INT, "status") or 0), _stream(dev)))
+    return None if k_values is None and v_values is None else (k_values, v_values)
 
 
 # ---------------------------------------------------------------- pages
@@ -344,19 +381,25 @@ def mqa_pages_fork(block_table, context_lens, parents, page_refs, *, page_size: 
     table entries point at each page) is recounted in place for the new table.
     Returns (out_table int32 [R, max_pages], out_lens int32 [R])."""
     B, R = block_table.shape[0], parents.numel()
-    with _Call(page_refs.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        if out_table is None:
-            out_table = call.empty((R, block_table.shape[1]), torch.int32)
-        if out_lens is None:
-            out_lens = call.empty((R,), torch.int32)
-        p = PagesParams(B, R, block_table.shape[1], page_refs.numel(), page_size, flags,
-                        call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_pages_fork(
-            table, lens, call.ptr(parents, "parents", torch.int32),
-            call.ptr(page_refs, "page_refs", torch.int32),
-            call.ptr(out_table, "out_table", torch.int32, shape=(R, block_table.shape[1])),
-            call.ptr(out_lens, "out_lens", torch.int32, numel=R), ctypes.byref(p), call.stream))
+    width = _width(block_table, B)
+    if _elsewhere(page_refs, stream):
+        with _there(page_refs, stream):
+            return mqa_pages_fork(block_table, context_lens, parents, page_refs,
+                                  page_size=page_size, out_table=out_table, out_lens=out_lens,
+                                  flags=flags, status=status)
+    dev = page_refs.get_device()
+    if out_table is None:
+        out_table = page_refs.new_empty((R, width), dtype=_INT)
+    if out_lens is None:
+        out_lens = page_refs.new_empty((R,), dtype=_INT)
+    _check(_lib().mqa_pages_fork(
+        _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"), _ptr(parents, dev, _INT, "parents"),
+        _ptr(page_refs, dev, _INT, "page_refs"),
+        _shaped(out_table, (R, width), dev, _INT, "out_table"),
+        _sized(out_lens, R, dev, _INT, "out_lens"),
+        _PAGES.pack(B, R, width, page_refs.numel(), page_size, flags,
+                    _ptr(status, dev, _INT, "status") or 0), _stream(dev)))
     return out_table, out_lens
 
 
@@ -371,19 +414,26 @@ def mqa_pages_resize(block_table, context_lens, new_lens, page_refs, *, page_siz
     Rows for which no pages were left keep their length (context_lens tells;
     MQA_STATUS_NO_PAGES)."""
     B = block_table.shape[0]
-    with _Call(page_refs.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        if copy_src is None:
-            copy_src = call.empty((B,), torch.int32)
-        if copy_dst is None:
-            copy_dst = call.empty((B,), torch.int32)
-        p = PagesParams(B, 0, block_table.shape[1], page_refs.numel(), page_size, flags,
-                        call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_pages_resize(
-            table, lens, call.ptr(new_lens, "new_lens", torch.int32, numel=B),
-            call.ptr(page_refs, "page_refs", torch.int32),
-            call.ptr(copy_src, "copy_src", torch.int32, numel=B),
-            call.ptr(copy_dst, "copy_dst", torch.int32, numel=B), ctypes.byref(p), call.stream))
+    width = _width(block_table, B)
+    if _elsewhere(page_refs, stream):
+        with _there(page_refs, stream):
+            return mqa_pages_resize(block_table, context_lens, new_lens, page_refs,
+                                    page_size=page_size, copy_src=copy_src, copy_dst=copy_dst,
+                                    flags=flags, status=status)
+    dev = page_refs.get_device()
+    if copy_src is None and copy_dst is None:
+        copy_src, copy_dst = page_refs.new_empty((2, B), dtype=_INT)
+    elif copy_src is None:
+        copy_src = torch.empty_like(copy_dst)
+    elif copy_dst is None:
+        copy_dst = torch.empty_like(copy_src)
+    _check(_lib().mqa_pages_resize(
+        _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"),
+        _sized(new_lens, B, dev, _INT, "new_lens"), _ptr(page_refs, dev, _INT, "page_refs"),
+        _sized(copy_src, B, dev, _INT, "copy_src"), _sized(copy_dst, B, dev, _INT, "copy_dst"),
+        _PAGES.pack(B, 0, width, page_refs.numel(), page_size, flags,
+                    _ptr(status, dev, _INT, "status") or 0), _stream(dev)))
     return copy_src, copy_dst
 
 
@@ -398,19 +448,24 @@ def mqa_pages_compact(block_table, context_lens, page_refs, *, page_size: int,
     first count[0] pairs are the copies to make (mqa_pages_copy with `count`), and
     page_map[p] is page p's new number, -1 for a free page."""
     B, P = block_table.shape[0], page_refs.numel()
-    with _Call(page_refs.device, stream) as call:
-        table, lens = _table(call, block_table, context_lens, B)
-        copy_src, copy_dst, count, page_map = (
-            call.empty((n,), torch.int32) if t is None else t
-            for t, n in ((copy_src, P // 2), (copy_dst, P // 2), (count, 1), (page_map, P)))
-        p = PagesParams(B, 0, block_table.shape[1], P, page_size, flags,
-                        call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_pages_compact(
-            table, lens, call.ptr(page_refs, "page_refs", torch.int32),
-            call.ptr(copy_src, "copy_src", torch.int32, numel=P // 2),
-            call.ptr(copy_dst, "copy_dst", torch.int32, numel=P // 2),
-            call.ptr(count, "count", torch.int32, numel=1),
-            call.ptr(page_map, "page_map", torch.int32, numel=P), ctypes.byref(p), call.stream))
+    width = _width(block_table, B)
+    if _elsewhere(page_refs, stream):
+        with _there(page_refs, stream):
+            return mqa_pages_compact(block_table, context_lens, page_refs, page_size=page_size,
+                                     copy_src=copy_src, copy_dst=copy_dst, count=count,
+                                     page_map=page_map, flags=flags, status=status)
+    dev = page_refs.get_device()
+    copy_src, copy_dst, count, page_map = (
+        page_refs.new_empty((n,), dtype=_INT) if t is None else t
+        for t, n in ((copy_src, P // 2), (copy_dst, P // 2), (count, 1), (page_map, P)))
+    _check(_lib().mqa_pages_compact(
+        _ptr(block_table, dev, _INT, "block_table"),
+        _sized(context_lens, B, dev, _INT, "context_lens"),
+        _ptr(page_refs, dev, _INT, "page_refs"), _sized(copy_src, P // 2, dev, _INT, "copy_src"),
+        _sized(copy_dst, P // 2, dev, _INT, "copy_dst"), _sized(count, 1, dev, _INT, "count"),
+        _sized(page_map, P, dev, _INT, "page_map"),
+        _PAGES.pack(B, 0, width, P, page_size, flags, _ptr(status, dev, _INT, "status") or 0),
+        _stream(dev)))
     return copy_src, copy_dst, count, page_map
 
 
@@ -422,22 +477,25 @@ def mqa_pages_copy(caches: Union[torch.Tensor, Sequence[torch.Tensor]], src, dst
     count[0] pairs."""
     if isinstance(caches, torch.Tensor):
         caches = (caches,)
-    caches = list(caches)
     if not caches:
         raise ValueError("give at least one cache")
     if src.shape != dst.shape:
         raise ValueError("src and dst must have one shape")
-    num_pages = caches[0].shape[0]
-    n = len(caches)
-    with _Call(caches[0].device, stream) as call:
-        ptrs, sizes = (_P * n)(), (_I64 * n)()
-        for i, c in enumerate(caches):
-            if c.dim() < 2 or c.shape[0] != num_pages:
-                raise ValueError(f"caches must all be [{num_pages}, ...]")
-            ptrs[i] = call.ptr(c, "cache", torch.uint8)
-            sizes[i] = c.numel() // max(num_pages, 1)
-        p = PagesParams(0, 0, 0, num_pages, 0, flags, call.ptr(status, "status", torch.int32))
-        _check(_lib().mqa_pages_copy(
-            ptrs, sizes, n, call.ptr(src, "src", torch.int32), call.ptr(dst, "dst", torch.int32),
-            src.numel(), call.ptr(count, "count", torch.int32, numel=1), ctypes.byref(p),
-            call.stream))
+    first = caches[0]
+    num_pages, n = first.shape[0], len(caches)
+    if _elsewhere(first, stream):
+        with _there(first, stream):
+            return mqa_pages_copy(caches, src, dst, count, flags=flags, status=status)
+    dev = first.get_device()
+    ptrs, sizes = [], []
+    for c in caches:
+        if c.dim() < 2 or c.shape[0] != num_pages:
+            raise ValueError(f"caches must all be [{num_pages}, ...]")
+        ptrs.append(_ptr(c, dev, _BYTE, "cache"))
+        sizes.append(c.numel() // max(num_pages, 1))
+    _check(_lib().mqa_pages_copy(
+        struct.pack(f"@{n}P", *ptrs), struct.pack(f"@{n}q", *sizes), n,
+        _ptr(src, dev, _INT, "src"), _ptr(dst, dev, _INT, "dst"), src.numel(),
+        _sized(count, 1, dev, _INT, "count"),
+        _PAGES.pack(0, 0, 0, num_pages, 0, flags, _ptr(status, dev, _INT, "status") or 0),
+        _stream(dev)))
