@@ -147,8 +147,15 @@ __global__ void __launch_bounds__(kThreads) append_fp4_kernel(AppendArgs a) {
     uint32_t sc = to_e4m3x2(__fdiv_rn(most, 6.f), 0.f) & 0xffu;
     if (sc == 0) sc = 1;  // 2^-9
     const float s = from_e4m3x2(sc).x;
+    // x / s by a product with 1 / s, which is off by less than 2^-22 of it, then rounded
+    // to 17 bits: x has at most 11 and s times a midpoint of e2m1 at most 7, so a
+    // quotient that is no midpoint lies 2^-11 of it or more away from each, and one
+    // that is becomes it again. (16 divisions instead took the kernel from 0.9 to 0.7 of
+    // the copy rate.)
+    const float inv = __fdiv_rn(1.f, s);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __fdiv_rn(v[k], s);
+    for (int k = 0; k < 16; ++k)
+        v[k] = __uint_as_float((__float_as_uint(v[k] * inv) + 0x40u) & 0xffffff80u);
     const uint2 code = make_uint2(to_e2m1x8(v), to_e2m1x8(v + 8));
     const int64_t head_bytes = (int64_t)a.page_size * (D / 2 + D / 16);
     uint8_t* block = static_cast<uint8_t*>(x.cache) + ((int64_t)p.page * a.heads + h) * head_bytes;

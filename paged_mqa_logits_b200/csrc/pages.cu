@@ -109,75 +109,105 @@ __global__ void __launch_bounds__(128) fork_kernel(const int32_t* table, const i
 }
 
 // ---------------------------------------------------------------- resize
-// One CTA. (1) every row's need of pages and the prefix sums over the rows; (2) a
-// scan of page_refs ranks the free pages, and the page of rank r goes to the row
-// whose range of ranks holds r; it ends once every need is met; (3) lengths,
-// releases and the counts of replaced pages (after the scan, so that nothing
-// freed here is taken here).
+// One CTA, since every step hangs on prefix sums over the rows or the pool and the
+// work is a few thousand entries. (1) every row's need of pages and the prefix sums
+// over the rows; (2) a scan of page_refs ranks the free pages, and the page of rank r
+// goes to the row whose range of ranks holds r; it ends once every need is met; (3)
+// lengths, releases and the counts of replaced pages (after the scan, so that nothing
+// freed here is taken here). What bounds it are chains of loads from L2: four rows or
+// eight pages a thread are loaded together, and the next pages while the present
+// ones are ranked.
+constexpr int kRows = 4;  // of a thread at a time in step 1
+
+// kCached: where the row's new pages start in its table, and whether the first of
+// them takes another's place, is kept in shared memory (else found again).
+template <bool kCached>
 __global__ void __launch_bounds__(kPlanThreads) resize_kernel(int32_t* table, int32_t* lens,
                                                               const int32_t* new_lens,
                                                               int32_t* refs, int32_t* src,
                                                               int32_t* dst, PagesArgs a) {
-    extern __shared__ int pre[];  // [batch + 1]: ranks before each row
+    extern __shared__ int pre[];             // [batch + 1]: ranks before each row
+    int* start = pre + a.batch + 1;          // [batch]: first new entry * 2 + (takes another's place)
     __shared__ int tmp[33];
     ptx::griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31;
     const int most = a.max_pages << a.ps_shift;
     int total = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int need = 0;
-        if (b < a.batch) {
-            const int old = len_of(a, lens, b), now = clamp_len(a.status, new_lens[b], most);
-            const int had = pages_of(a, old);
-            int shared = -1;
-            if (now > old) {
-                need = pages_of(a, now) - had;
-                if (old & (a.page_size - 1)) {
-                    const int p = table[(int64_t)b * a.max_pages + had - 1];
-                    if (good_page(a, p) && refs[p] > 1) {
-                        shared = p;
-                        ++need;
-                    }
-                }
-            }
-            src[b] = shared;
-            dst[b] = -1;
+    for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads * kRows) {
+        int old[kRows], now[kRows], end[kRows], need[kRows], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int b = b0 + tid * kRows + i;
+            old[i] = b < a.batch ? lens[b] : 0;
+            now[i] = b < a.batch ? new_lens[b] : 0;
         }
-        int sum;
-        const int before = block_scan(need, tmp, sum);
-        if (b < a.batch) pre[b] = total + before;
-        total += sum;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int b = b0 + tid * kRows + i;
+            old[i] = clamp_len(a.status, old[i], most);
+            now[i] = clamp_len(a.status, now[i], most);
+            end[i] = now[i] > old[i] && (old[i] & (a.page_size - 1))
+                         ? table[(int64_t)b * a.max_pages + pages_of(a, old[i]) - 1] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const bool partly = now[i] > old[i] && (old[i] & (a.page_size - 1));
+            if (!partly || !good_page(a, end[i]) || refs[end[i]] <= 1) end[i] = -1;
+            need[i] = (now[i] > old[i] ? pages_of(a, now[i]) - pages_of(a, old[i]) : 0) + (end[i] >= 0);
+            sum += need[i];
+        }
+        int all;
+        int before = total + block_scan(sum, tmp, all);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int b = b0 + tid * kRows + i;
+            if (b >= a.batch) break;
+            src[b] = end[i];
+            dst[b] = -1;
+            pre[b] = before;
+            if (kCached) start[b] = (pages_of(a, old[i]) - (end[i] >= 0)) * 2 + (end[i] >= 0);
+            before += need[i];
+        }
+        total += all;
     }
     if (tid == 0) pre[a.batch] = total;
     __syncthreads();
+    auto start_of = [&](int b) {
+        if (kCached) return start[b];
+        const int swaps = src[b] >= 0;
+        return (pages_of(a, len_of(a, lens, b)) - swaps) * 2 + swaps;
+    };
 
     int found = 0;
+    int r[kPer];
+    if (total > 0) load_refs(refs, tid * kPer, a.num_pages, r);
     for (int p0 = 0; p0 < a.num_pages && found < total; p0 += kRound) {
-        int r[kPer], free = 0, sum;
-        load_refs(refs, p0 + tid * kPer, a.num_pages, r);
+        int free = 0, sum, next[kPer];
+        load_refs(refs, p0 + kRound + tid * kPer, a.num_pages, next);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) free += r[i] == 0;
         int rank = found + block_scan(free, tmp, sum);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (r[i] != 0) continue;
-            if (rank < total) {
-                const int page = p0 + tid * kPer + i;
-                int lo = 0, hi = a.batch - 1;  // the last row that begins at or before rank
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (pre[mid] <= rank) lo = mid; else hi = mid - 1;
-                }
-                const bool swaps = src[lo] >= 0;
-                const int at = pages_of(a, len_of(a, lens, lo)) + rank - pre[lo] - (swaps ? 1 : 0);
-                table[(int64_t)lo * a.max_pages + at] = page;
-                if (swaps && rank == pre[lo]) dst[lo] = page;
-                refs[page] = 1;
+        if (free > 0 && rank < total) {
+            int lo = 0, hi = a.batch - 1;  // the last row that begins at or before rank
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] <= rank) lo = mid; else hi = mid - 1;
             }
-            ++rank;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (r[i] != 0 || rank >= total) continue;
+                const int page = p0 + tid * kPer + i;
+                while (pre[lo + 1] <= rank) ++lo;
+                const int at = start_of(lo);
+                table[(int64_t)lo * a.max_pages + (at >> 1) + rank - pre[lo]] = page;
+                if ((at & 1) && rank == pre[lo]) dst[lo] = page;
+                refs[page] = 1;
+                ++rank;
+            }
         }
         found += sum;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) r[i] = next[i];
     }
     __syncthreads();
     if (found < total) {
@@ -185,12 +215,11 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(int32_t* table, in
         for (int b = tid; b < a.batch; b += kPlanThreads) {
             if (pre[b + 1] == pre[b] || pre[b + 1] <= found) continue;
             // at most one row was given a part of its pages: they go back
-            const int had = pages_of(a, len_of(a, lens, b)) - (src[b] >= 0 ? 1 : 0);
-            int32_t* row = table + (int64_t)b * a.max_pages;
-            for (int r = pre[b]; r < found; ++r) {
-                const int at = had + r - pre[b];
-                refs[row[at]] = 0;
-                row[at] = r == pre[b] && src[b] >= 0 ? src[b] : -1;
+            const int at = start_of(b);
+            int32_t* row = table + (int64_t)b * a.max_pages + (at >> 1);
+            for (int k = pre[b]; k < found; ++k) {
+                refs[row[k - pre[b]]] = 0;
+                row[k - pre[b]] = k == pre[b] && (at & 1) ? src[b] : -1;
             }
             src[b] = -1;
             dst[b] = -1;
@@ -202,13 +231,14 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(int32_t* table, in
         const int b = b0 + lane;
         int had = 0, has = 0;
         if (b < a.batch) {
-            const int old = len_of(a, lens, b);
-            int now = clamp_len(a.status, new_lens[b], most);
-            if (pre[b + 1] > found && pre[b + 1] > pre[b]) now = old;
-            had = pages_of(a, old);
-            has = pages_of(a, now);
-            if (src[b] >= 0) atomicSub(refs + src[b], 1);
+            const int old = lens[b], want = new_lens[b], from = src[b];
+            had = min(max(old, 0), most);
+            int now = min(max(want, 0), most);
+            if (pre[b + 1] > found && pre[b + 1] > pre[b]) now = had;
+            if (from >= 0) atomicSub(refs + from, 1);
             lens[b] = now;
+            had = pages_of(a, had);
+            has = pages_of(a, now);
         }
         uint32_t shrinks = __ballot_sync(0xffffffffu, has < had);
         while (shrinks) {
@@ -234,14 +264,22 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int32_t* ref
     ptx::griddep_wait();
     const int tid = threadIdx.x, half = a.num_pages / 2;
     int live = 0;
-    for (int p = tid; p < a.num_pages; p += kPlanThreads) live += refs[p] > 0;
+#pragma unroll 4
+    for (int first = tid * kPer; first < a.num_pages; first += kRound) {
+        int r[kPer];
+        load_refs(refs, first, a.num_pages, r);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) live += first + i < a.num_pages && r[i] > 0;
+    }
     int n;
     block_scan(live, tmp, n);
     int moves = 0, holes = 0;
+    int r[kPer];
+    load_refs(refs, tid * kPer, a.num_pages, r);
     for (int p0 = 0; p0 < a.num_pages; p0 += kRound) {
-        int r[kPer], m = 0, h = 0, sum;
+        int m = 0, h = 0, sum, next[kPer];
         const int first = p0 + tid * kPer;
-        load_refs(refs, first, a.num_pages, r);
+        load_refs(refs, first + kRound, a.num_pages, next);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int p = first + i;
@@ -261,18 +299,32 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int32_t* ref
         }
         moves += sum & 0xffff;
         holes += sum >> 16;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) r[i] = next[i];
     }
     __syncthreads();
-    for (int i = tid; i < half; i += kPlanThreads) {
-        if (i < moves) {
-            const int s = src[i], d = dst[i];
-            map[s] = d;
-            refs[d] = refs[s];
-            refs[s] = 0;
-        } else {
-            src[i] = -1;
-            dst[i] = -1;
+    for (int i0 = 0; i0 < moves; i0 += kRound) {
+        int s[kPer], d[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int i = i0 + k * kPlanThreads + tid;
+            s[k] = i < moves ? src[i] : -1;
+            d[k] = i < moves ? dst[i] : -1;
         }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (s[k] >= 0) r[k] = refs[s[k]];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (s[k] >= 0) {
+                map[s[k]] = d[k];
+                refs[d[k]] = r[k];
+                refs[s[k]] = 0;
+            }
+    }
+    for (int i = moves + tid; i < half; i += kPlanThreads) {
+        src[i] = -1;
+        dst[i] = -1;
     }
     if (tid == 0) *count = moves;
 }
@@ -288,31 +340,41 @@ __global__ void __launch_bounds__(128) compact_table_kernel(int32_t* table, cons
 }
 
 // ---------------------------------------------------------------- copy
-constexpr int kCopyThreads = 256;
+// A warp copies a page of one cache at a time, four 16-byte pieces a lane in flight;
+// the pairs of the warp's next page are loaded meanwhile. (A CTA a page left half of its
+// threads idle on pages of 2 KB: 0.77 of the copy rate instead of the figure below.)
+constexpr int kCopyThreads = 256, kCopyWarps = kCopyThreads / 32;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
     ptx::griddep_wait();
     const int n = a.count != nullptr ? min(max(*a.count, 0), a.n) : a.n;
     const uint32_t chunks = a.chunks[blockIdx.y];
-    uint4* pool = static_cast<uint4*>(a.cache[blockIdx.y]);
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
-        const int s = a.src[i], d = a.dst[i];
-        if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages) {
-            if ((s != -1 || d != -1) && threadIdx.x == 0)
-                report_checked(a.status, MQA_STATUS_BAD_PAGE);
-            continue;
-        }
-        const uint4* from = pool + (int64_t)s * chunks;
-        uint4* to = pool + (int64_t)d * chunks;
-        uint32_t c = threadIdx.x;
-        for (; c + 3 * kCopyThreads < chunks; c += 4 * kCopyThreads) {
-            uint4 v[4];
+    const uint32_t lane = threadIdx.x & 31;
+    uint4* const pool = static_cast<uint4*>(a.cache[blockIdx.y]);
+    const int step = gridDim.x * kCopyWarps;
+    int i = blockIdx.x * kCopyWarps + (threadIdx.x >> 5);
+    int s = i < n ? a.src[i] : -1, d = i < n ? a.dst[i] : -1;
+    while (i < n) {
+        const int next = i + step;
+        const int s1 = next < n ? a.src[next] : -1, d1 = next < n ? a.dst[next] : -1;
+        if (s >= 0 && s < a.num_pages && d >= 0 && d < a.num_pages) {
+            const uint4* from = pool + (int64_t)s * chunks;
+            uint4* to = pool + (int64_t)d * chunks;
+            for (uint32_t c = lane; c < chunks; c += 128) {
+                uint4 v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = from[c + k * kCopyThreads];
+                for (int k = 0; k < 4; ++k)
+                    if (c + 32 * k < chunks) v[k] = __ldcs(from + c + 32 * k);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[c + k * kCopyThreads] = v[k];
+                for (int k = 0; k < 4; ++k)
+                    if (c + 32 * k < chunks) __stcs(to + c + 32 * k, v[k]);
+            }
+        } else if ((s != -1 || d != -1) && lane == 0) {
+            report_checked(a.status, MQA_STATUS_BAD_PAGE);
         }
-        for (; c < chunks; c += kCopyThreads) to[c] = from[c];
+        i = next;
+        s = s1;
+        d = d1;
     }
 }
 
@@ -328,14 +390,17 @@ cudaError_t launch_fork(const int32_t* table, const int32_t* lens, const int32_t
 cudaError_t launch_resize(int device, int32_t* table, int32_t* lens, const int32_t* new_lens,
                           int32_t* refs, int32_t* src, int32_t* dst, const PagesArgs& a,
                           void* stream, bool pdl) {
-    static uint32_t done[64];
-    const uint32_t smem = (uint32_t)(a.batch + 1) * 4;
+    static uint32_t done[2][64];
+    const uint32_t pre = (uint32_t)(a.batch + 1) * 4;
+    const bool cached = pre * 2 <= 200000;
+    const uint32_t smem = cached ? pre * 2 : pre;
     if (smem > 40000) {
-        const cudaError_t e = allow_smem(resize_kernel, device, smem, done);
+        const cudaError_t e = cached ? allow_smem(resize_kernel<true>, device, smem, done[1])
+                                     : allow_smem(resize_kernel<false>, device, smem, done[0]);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(resize_kernel, dim3(1), dim3(kPlanThreads), smem, stream, pdl, table, lens,
-                      new_lens, refs, src, dst, a);
+    return launch_pdl(cached ? resize_kernel<true> : resize_kernel<false>, dim3(1),
+                      dim3(kPlanThreads), smem, stream, pdl, table, lens, new_lens, refs, src, dst, a);
 }
 
 cudaError_t launch_compact(int32_t* table, const int32_t* lens, int32_t* refs, int32_t* src,
@@ -349,8 +414,10 @@ cudaError_t launch_compact(int32_t* table, const int32_t* lens, int32_t* refs, i
 }
 
 cudaError_t launch_copy(const CopyArgs& a, void* stream, bool pdl) {
-    const int x = a.n < 4096 ? a.n : 4096;
-    return launch_pdl(copy_kernel, dim3(x, a.num_caches), dim3(kCopyThreads), 0, stream, pdl, a);
+    // as many CTAs as the SMs hold at once, over all caches
+    const int most = (148 * 6 + a.num_caches - 1) / a.num_caches;
+    const int want = (int)(((int64_t)a.n + kCopyWarps - 1) / kCopyWarps);
+    return launch_pdl(copy_kernel, dim3(want < most ? want : most, a.num_caches), dim3(kCopyThreads), 0, stream, pdl, a);
 }
 
 }  // namespace mqa
