@@ -70,9 +70,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     ptx::griddep_wait();
 
-    if constexpr (!kList) {
-        if (blockIdx.y == 0) dense_extras<D>(a, warp, lane);
-    }
 
     int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
     const int pairs_end = pair + a.kv_heads;
@@ -372,6 +369,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } while (pair < pairs_end && !kList);
+    if constexpr (!kList) {
+        if (blockIdx.y == 0) dense_extras<D>(a, warp, kWarps, lane);
+    }
 }
 
 // ---------------------------------------------------------------- combine

@@ -237,8 +237,9 @@ __device__ __forceinline__ bool row_is_whole(const AttentionArgs& a, const Range
 
 // What every dense launch does besides: the schedule's check in validate mode, and
 // the results of rows without tokens, which are in no CTA's range.
+// `warp` of the `warps` that do it.
 template <int D>
-__device__ __forceinline__ void dense_extras(const AttentionArgs& a, int warp, int lane) {
+__device__ __forceinline__ void dense_extras(const AttentionArgs& a, int warp, int warps, int lane) {
     if ((a.status.flags & MQA_FLAG_VALIDATE) && warp == 0) {
         KernelArgs ka{};
         ka.context_lens = a.context_lens;
@@ -252,10 +253,10 @@ __device__ __forceinline__ void dense_extras(const AttentionArgs& a, int warp, i
     for (int b = blockIdx.x; b < a.batch; b += a.num_ctas) {
         if (__ldg(a.context_lens + b) > 0) continue;
         const int64_t o = (int64_t)b * a.next_n * a.heads;
-        for (int j = threadIdx.x; j < a.next_n * a.heads * (D / 8); j += blockDim.x)
+        for (int j = warp * 32 + lane; j < a.next_n * a.heads * (D / 8); j += warps * 32)
             reinterpret_cast<uint4*>(a.out)[o * (D / 8) + j] = make_uint4(0, 0, 0, 0);
         if (a.lse != nullptr)
-            for (int j = threadIdx.x; j < a.next_n * a.heads; j += blockDim.x) a.lse[o + j] = -INFINITY;
+            for (int j = warp * 32 + lane; j < a.next_n * a.heads; j += warps * 32) a.lse[o + j] = -INFINITY;
     }
 }
 

@@ -219,25 +219,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == kMmaWarp) ptx::tmem_alloc(&bars->tmem, kColumns);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&bars->k_full[i], kDequantWarps);
-            ptx::mbar_init(&bars->v_full[i], kDequantWarps);
-            ptx::mbar_init(&bars->pv_done[i], 1);
-            for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[q][i], 1);
-        }
-        for (int i = 0; i < kBufS; ++i) {
-            ptx::mbar_init(&bars->s_full[i], 1);
-            ptx::mbar_init(&bars->p_full[i], kSoftmaxWarps / 2);
-            ptx::mbar_init(&bars->s_free[i], 1);
-        }
-        ptx::mbar_init(&bars->q_full, kSoftmaxWarps);
-        for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->pair[q], 2);
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&bars->copies[i], kSoftmaxWarps / 2);
-            ptx::mbar_init(&bars->drain[i], 1);
-        }
-        bars->abort = 0;
+    if (warp == kSoftmaxWarp) {
+        // a lane a barrier
+        uint64_t* bar = nullptr;
+        uint32_t arrivals = 1;
+        if (lane < 2) bar = &bars->k_full[lane], arrivals = kDequantWarps;
+        else if (lane < 4) bar = &bars->v_full[lane - 2], arrivals = kDequantWarps;
+        else if (lane < 6) bar = &bars->pv_done[lane - 4];
+        else if (lane < 9) bar = &bars->s_full[lane - 6];
+        else if (lane < 12) bar = &bars->p_full[lane - 9], arrivals = kSoftmaxWarps / 2;
+        else if (lane < 15) bar = &bars->s_free[lane - 12];
+        else if (lane < 23) bar = &bars->turn[0][0] + (lane - 15);
+        else if (lane < 27) bar = &bars->pair[lane - 23], arrivals = 2;
+        else if (lane < 29) bar = &bars->copies[lane - 27], arrivals = kSoftmaxWarps / 2;
+        else if (lane < 31) bar = &bars->drain[lane - 29];
+        else bar = &bars->q_full, arrivals = kSoftmaxWarps;
+        ptx::mbar_init(bar, arrivals);
+        if (lane == 0) bars->abort = 0;
         ptx::fence_mbar_init();
     }
     ptx::tc_fence_before();
@@ -246,7 +244,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     constexpr uint32_t tmem = kTmem;
 
     ptx::griddep_wait();
-    if constexpr (!kList) dense_extras<D>(a, warp, lane);
 
     int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
     const int pairs_end = pair + a.kv_heads;
@@ -705,6 +702,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 next_row<kList>(a, r);
             }
         } while (ok && pair < pairs_end && !kList);
+    }
+
+    if constexpr (!kList) {
+        if (warp == 2 || warp == 3) dense_extras<D>(a, warp - 2, 2, lane);
     }
 
     ptx::tc_fence_before();

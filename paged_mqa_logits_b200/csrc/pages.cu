@@ -5,6 +5,8 @@
 // the atomics on page_refs only add, so no result depends on thread order.
 #include "pages.cuh"
 
+#include <cooperative_groups.h>
+
 #include "host.cuh"
 
 namespace mqa {
@@ -255,36 +257,69 @@ __global__ void __launch_bounds__(kPlanThreads) resize_kernel(int32_t* table, in
 }
 
 // ---------------------------------------------------------------- compact
-// One CTA: counts the pages in use (N), ranks the used pages at N and above and
-// the free ones below N, pairs them, and moves the counts.
+// A cluster of 8 CTAs, each with a contiguous eighth of the pool: counts the pages in
+// use (N), then the used pages at N and above and the free ones below N, ranks both
+// (the eighths' counts go through distributed shared memory), pairs them, and moves
+// the counts. (One CTA took 26 us for 22 thousand pages.)
+constexpr int kPlanCtas = 8;
+
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int32_t* refs, int32_t* src,
                                                                     int32_t* dst, int32_t* count,
                                                                     int32_t* map, PagesArgs a) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
     __shared__ int tmp[33];
+    __shared__ int mine[3];  // this CTA's pages in use; to move; holes to fill
     ptx::griddep_wait();
-    const int tid = threadIdx.x, half = a.num_pages / 2;
-    int live = 0;
-#pragma unroll 4
-    for (int first = tid * kPer; first < a.num_pages; first += kRound) {
-        int r[kPer];
-        load_refs(refs, first, a.num_pages, r);
+    const int tid = threadIdx.x, half = a.num_pages / 2, rank = (int)cluster.block_rank();
+    const int per = ((a.num_pages + kPlanCtas - 1) / kPlanCtas + kPer - 1) / kPer * kPer;
+    const int begin = (int)min((int64_t)rank * per, (int64_t)a.num_pages), end = min(a.num_pages - begin, per) + begin;
+    auto counts = [&](int n, int& m, int& h) {  // of the slice, per thread: n < 0: the pages in use
+        m = h = 0;
+        for (int first = begin + tid * kPer; first < end; first += kRound) {
+            int r[kPer];
+            load_refs(refs, first, a.num_pages, r);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) live += first + i < a.num_pages && r[i] > 0;
+            for (int i = 0; i < kPer; ++i) {
+                const int p = first + i;
+                const bool live = r[i] > 0;
+                m += p < end && live && (n < 0 || p >= n);
+                h += p < end && p < n && !live;
+            }
+        }
+    };
+    int m, h, live, n = 0;
+    counts(-1, m, h);
+    block_scan(m, tmp, live);
+    if (tid == 0) mine[0] = live;
+    cluster.sync();
+    for (int c = 0; c < kPlanCtas; ++c) n += *cluster.map_shared_rank(&mine[0], c);
+    int all_m, all_h;
+    counts(n, m, h);
+    block_scan(m, tmp, all_m);
+    block_scan(h, tmp, all_h);
+    if (tid == 0) {
+        mine[1] = all_m;
+        mine[2] = all_h;
     }
-    int n;
-    block_scan(live, tmp, n);
-    int moves = 0, holes = 0;
-    int r[kPer];
-    load_refs(refs, tid * kPer, a.num_pages, r);
-    for (int p0 = 0; p0 < a.num_pages; p0 += kRound) {
-        int m = 0, h = 0, sum, next[kPer];
+    cluster.sync();
+    int moves = 0, holes = 0, total = 0;
+    for (int c = 0; c < kPlanCtas; ++c) {
+        const int cm = *cluster.map_shared_rank(&mine[1], c), ch = *cluster.map_shared_rank(&mine[2], c);
+        moves += c < rank ? cm : 0;
+        holes += c < rank ? ch : 0;
+        total += cm;
+    }
+    for (int p0 = begin; p0 < end; p0 += kRound) {
         const int first = p0 + tid * kPer;
-        load_refs(refs, first + kRound, a.num_pages, next);
+        int r[kPer], sum;
+        load_refs(refs, first, a.num_pages, r);
+        m = h = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int p = first + i;
-            m += p < a.num_pages && p >= n && r[i] > 0;
-            h += p < n && r[i] <= 0;
+            m += p < end && p >= n && r[i] > 0;
+            h += p < end && p < n && r[i] <= 0;
         }
         // both counts stay below 2^16 a round: one scan for the two
         const int both = block_scan(m | h << 16, tmp, sum);
@@ -292,41 +327,30 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(int32_t* ref
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int p = first + i;
-            if (p >= a.num_pages) break;
+            if (p >= end) break;
             if (p >= n && r[i] > 0) src[mr++] = p;
             if (p < n && r[i] <= 0) dst[hr++] = p;
             map[p] = r[i] > 0 ? p : -1;
         }
         moves += sum & 0xffff;
         holes += sum >> 16;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) r[i] = next[i];
     }
-    __syncthreads();
-    for (int i0 = 0; i0 < moves; i0 += kRound) {
-        int s[kPer], d[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = i0 + k * kPlanThreads + tid;
-            s[k] = i < moves ? src[i] : -1;
-            d[k] = i < moves ? dst[i] : -1;
+    cluster.sync();
+    const int threads = kPlanCtas * kPlanThreads;
+    for (int i = rank * kPlanThreads + tid; i < half; i += threads) {
+        if (i < total) {
+            const int s = src[i], d = dst[i];
+            const int r = refs[s];
+            map[s] = d;
+            refs[d] = r;
+            refs[s] = 0;
+        } else {
+            src[i] = -1;
+            dst[i] = -1;
         }
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (s[k] >= 0) r[k] = refs[s[k]];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (s[k] >= 0) {
-                map[s[k]] = d[k];
-                refs[d[k]] = r[k];
-                refs[s[k]] = 0;
-            }
     }
-    for (int i = moves + tid; i < half; i += kPlanThreads) {
-        src[i] = -1;
-        dst[i] = -1;
-    }
-    if (tid == 0) *count = moves;
+    if (rank == 0 && tid == 0) *count = total;
+    cluster.sync();  // no CTA ends while another may read its counts
 }
 
 __global__ void __launch_bounds__(128) compact_table_kernel(int32_t* table, const int32_t* lens,
@@ -406,8 +430,18 @@ cudaError_t launch_resize(int device, int32_t* table, int32_t* lens, const int32
 cudaError_t launch_compact(int32_t* table, const int32_t* lens, int32_t* refs, int32_t* src,
                            int32_t* dst, int32_t* count, int32_t* map, const PagesArgs& a,
                            void* stream, bool pdl) {
-    cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pdl,
-                               refs, src, dst, count, map, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPlanCtas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {kPlanCtas, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, compact_plan_kernel, refs, src, dst, count, map, a);
     if (e != cudaSuccess || a.batch == 0) return e;
     return launch_pdl(compact_table_kernel, dim3(a.batch), dim3(128), 0, stream, pdl, table, lens,
                       map, a);
