@@ -180,7 +180,7 @@ int paged_mqa_attention_fp4(const void* q, const void* k_cache, const void* v_ca
     a.ps_shift = log2_of(p.page_size);
     a.num_pages = p.num_pages;
     a.max_pages = p.max_pages_per_row;
-    a.page_bytes = (int64_t)p.num_kv_heads * p.page_size * (p.head_dim / 2 + p.head_dim / 16);
+    a.page_bytes = (uint32_t)p.num_kv_heads * p.page_size * (p.head_dim / 2 + p.head_dim / 16);
     a.status = {lib_status, p.status, with_env(p.flags)};
     a.scale_log2 = p.softmax_scale * 1.44269504088896f;
     const cudaError_t e = launch_attention(dev, p.head_dim, p.dtype, a, stream,

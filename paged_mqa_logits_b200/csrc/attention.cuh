@@ -19,7 +19,7 @@ struct AttentionArgs {
     float* part_o;            // [slots][Hk][rows][D]
     float* part_ml;           // [slots][Hk][rows][4]: maximum, sum, sum of unrounded p
     int64_t q_sb, q_sn, q_sh; // strides of q in elements
-    int64_t page_bytes;       // of one cache: Hk heads
+    uint32_t page_bytes;      // of one cache: Hk heads
     StatusWords status;
     float scale_log2;         // softmax_scale * log2(e)
     int32_t batch, next_n, heads, kv_heads, group;

@@ -267,16 +267,17 @@ template <int D, int kStep, bool kList, bool kTile>
 struct SpanLoader {
     static constexpr int kRow = D / 2, kScales = D / 16;
     Range r;
-    const int32_t* list;
-    int64_t head_at;
+    const int32_t* list;   // selected: the row's token list
+    const int32_t* table;  // the row's block table
+    uint32_t head_at;
     int lane, off, pos;
-    // This lane's token of the span to be copied next, found a step ahead: its token
+    // This lane's token of the span to be copied next, found a step ahead: the token
     // (-1 for none), its page as loaded (not looked at before the copy, so that nothing
-    // waits for the load), and if there is a span at all.
+    // waits for the load), whether there is a span at all, and whether it is whole: 32
+    // neighbouring tokens of one page.
     int tok, page;
-    bool any;
+    bool any, whole;
     int ahead;      // selected: the list's entry for the span after that, as loaded
-    int slot;       // in copy(): the token's cache slot (page * page_size + slot), -1 for none
     uint32_t seen;  // selected: lane s keeps the mask of the visible tokens in ring slot s
 
     __device__ __forceinline__ void open(const AttentionArgs& a, const Range& range, int lane_, int off_) {
@@ -285,7 +286,8 @@ struct SpanLoader {
         off = off_;
         pos = r.w.t0 + off;
         list = kList ? a.indices + (int64_t)r.w.item * a.topk : nullptr;
-        head_at = (int64_t)r.hk * a.page_size * (kRow + kScales);
+        table = a.block_table + (int64_t)min(r.w.b, a.batch - 1) * a.max_pages;
+        head_at = (uint32_t)r.hk * a.page_size * (kRow + kScales);
         seen = 0;
         if constexpr (kList) ahead = pos + lane < r.w.t1 ? __ldg(list + pos + lane) : -1;
         resolve(a);
@@ -297,10 +299,12 @@ struct SpanLoader {
         while (r.more && (kTile ? pos - off : pos) >= r.w.t1) {
             next_row<kList>(a, r);
             pos = r.w.t0 + off;
+            table = a.block_table + (int64_t)min(r.w.b, a.batch - 1) * a.max_pages;
         }
         if (!r.more) return;
         any = true;
         const int t = pos + lane;
+        whole = !kList && pos + kSpan <= r.w.t1 && a.page_size >= kSpan;
         pos += kStep;
         if constexpr (kList) {
             tok = ahead >= 0 && ahead < r.w.ctx ? ahead : -1;
@@ -308,7 +312,7 @@ struct SpanLoader {
         } else {
             tok = t < r.w.t1 ? t : -1;
         }
-        page = __ldg(a.block_table + (int64_t)r.w.b * a.max_pages + (max(tok, 0) >> a.ps_shift));
+        page = __ldg(table + (max(tok, 0) >> a.ps_shift));
     }
 
     // Copies the span's codes and scales of `caches` caches (K, then V, to slots
@@ -319,19 +323,16 @@ struct SpanLoader {
                                          uint32_t stride, uint32_t scales, uint32_t scale_stride) {
         constexpr int kPieces = kRow / 16;  // 16-byte pieces of a token's codes
         auto place = [](int t, int o) { return kTile ? tile_at<D>(t, o) : code_at<D>(t, o); };
-        if (page < 0 || page >= a.num_pages) {
+        if ((uint32_t)page >= (uint32_t)a.num_pages) {
             if (tok >= 0) report_checked(a.status, MQA_STATUS_BAD_PAGE);
             page = page < 0 ? 0 : a.num_pages - 1;
         }
-        slot = tok >= 0 ? (page << a.ps_shift) | (tok & (a.page_size - 1)) : -1;
-        const bool whole = __all_sync(0xffffffffu, slot >= 0);
-        if (!kList && whole && a.page_size >= kSpan) {
-            // one stretch of one page
-            const int first = __shfl_sync(0xffffffffu, slot, 0);
-            const int in = first & (a.page_size - 1);
-            const int64_t page = (int64_t)(first >> a.ps_shift) * a.page_bytes + head_at;
-            const int64_t from = page + in * kRow + lane * 16;
-            const int64_t sc = page + a.page_size * kRow + (in + lane) * kScales;
+        const uint32_t in = (uint32_t)max(tok, 0) & (a.page_size - 1);
+        const int64_t at = (int64_t)page * a.page_bytes + head_at;  // of the page and head
+        const int64_t sc = at + (a.page_size * kRow + in * kScales);
+        if (whole) {
+            // one stretch of one page: this lane's piece i is 512 i bytes behind its first
+            const int64_t from = at + (in - lane) * kRow + lane * 16;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const uint32_t to = base + place((i * 32 + lane) / kPieces, (i * 32 + lane) % kPieces * 16);
@@ -341,21 +342,17 @@ struct SpanLoader {
             copy_async_all<kScales>(base + scales + lane * kScales, c0 + sc);
             if (kCaches == 2) copy_async_all<kScales>(base + scales + scale_stride + lane * kScales, c1 + sc);
         } else {
-            const int at = max(slot, 0);
-            const int64_t page = (int64_t)(at >> a.ps_shift) * a.page_bytes + head_at;
-            const int64_t mine = page + (at & (a.page_size - 1)) * kRow;
-            const int64_t sc = page + a.page_size * kRow + (at & (a.page_size - 1)) * kScales;
+            const int64_t mine = tok >= 0 ? at + in * kRow : -1;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int p = i * 32 + lane, t = p / kPieces, o = (p % kPieces) * 16;
-                const int64_t from = __shfl_sync(0xffffffffu, mine, t) + o;
-                const bool take = __shfl_sync(0xffffffffu, slot, t) >= 0;
+                const int64_t from = __shfl_sync(0xffffffffu, mine, t);
                 const uint32_t to = base + place(t, o);
-                copy_async<16>(to, c0 + from, take);
-                if (kCaches == 2) copy_async<16>(to + stride, c1 + from, take);
+                copy_async<16>(to, c0 + max(from, (int64_t)0) + o, from >= 0);
+                if (kCaches == 2) copy_async<16>(to + stride, c1 + max(from, (int64_t)0) + o, from >= 0);
             }
-            copy_async<kScales>(base + scales + lane * kScales, c0 + sc, slot >= 0);
-            if (kCaches == 2) copy_async<kScales>(base + scales + scale_stride + lane * kScales, c1 + sc, slot >= 0);
+            copy_async<kScales>(base + scales + lane * kScales, c0 + sc, tok >= 0);
+            if (kCaches == 2) copy_async<kScales>(base + scales + scale_stride + lane * kScales, c1 + sc, tok >= 0);
         }
     }
 
@@ -371,7 +368,7 @@ struct SpanLoader {
         if (any) {
             copy<2>(a, a.k, a.v, base, kSpan * kRow, 2 * kSpan * kRow, kSpan * kScales);
             if constexpr (kList) {
-                const uint32_t m = __ballot_sync(0xffffffffu, slot >= 0);
+                const uint32_t m = __ballot_sync(0xffffffffu, tok >= 0);
                 if (lane == stage) seen = m;
             }
         }
