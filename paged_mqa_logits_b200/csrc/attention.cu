@@ -13,16 +13,20 @@
 // The query rows are N, so 8 rows cost 8 and not 16. At the end of a row the CTA's
 // warps join their (m, sum, O) through shared memory; rows that several CTAs share
 // leave partial results, which combine_kernel joins.
+#include <algorithm>
+
 #include "attention_walk.cuh"
 #include "host.cuh"
 
 namespace mqa {
 namespace {
 
-// NT: query rows of a CTA / 8. More rows take more registers, so fewer warps.
-template <int D, int NT>
+// NT: query rows of a CTA / 8. More rows take more registers, so fewer warps. kFew: CTAs
+// of 4 warps, several to an SM, for short lists.
+template <int D, int NT, bool kFew>
 struct Shape {
-    static constexpr int kWarps = NT == 1 ? 16 : 12;
+    static constexpr int kWarps = kFew ? 4 : NT == 1 ? 16 : 12;
+    static constexpr int kPerSm = kFew ? (NT == 1 ? 4 : 3) : 1;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRow = D / 2;                       // code bytes of a token
     static constexpr int kScales = D / 16;                   // scale bytes of a token
@@ -34,7 +38,7 @@ struct Shape {
     static constexpr int kRows = 8 * NT;
     static constexpr int kRed = kWarps * kRows * kRedRow * 4;
     static constexpr int kSmem = kRing + kRed + kWarps * kRows * 4 * 4;
-    static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
+    static_assert(kPerSm * (kSmem + 1024) <= 233472, "more shared memory than an SM has");
 };
 
 // d += a (16 x 16) * b (16 x 8), f16 operands, fp32 accumulation.
@@ -54,9 +58,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-template <int D, int NT, typename T, bool kList>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(const AttentionArgs a) {
-    using S = Shape<D, NT>;
+template <int D, int NT, typename T, bool kList, bool kFew>
+__global__ void __launch_bounds__(Shape<D, NT, kFew>::kThreads, Shape<D, NT, kFew>::kPerSm)
+attention_kernel(const AttentionArgs a) {
+    using S = Shape<D, NT, kFew>;
     constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
     constexpr int kTiles = D / 16;   // row tiles of O^T, and contraction steps of K Q^T
     constexpr int kElems = D / 4;    // elements of a row of q or K that one lane of a quad holds
@@ -70,11 +75,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
 
     ptx::griddep_wait();
 
-
-    int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
-    const int pairs_end = pair + a.kv_heads;
+    __shared__ int parts;
+    if (!kList) {
+        const int n = parts_with_rows(a, lane);
+        if (threadIdx.x == 0) parts = n;
+        __syncthreads();
+    }
+    int pair = kList ? 0 : first_pair(a, parts, blockIdx.x);  // dense: the next (head, part) pair
+    bool last;
     do {
-        Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
+        Range r = open_range<kList>(a, blockIdx.x, parts, pair, last);
         const Walk& w = r.w;
         const int hk = r.hk, draft = r.draft;
         SpanLoader<D, kWarps * kSpan, kList, false> loads;
@@ -89,7 +99,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             // largest element lies in [2^14, 2^15)
             uint32_t qf[NT][kElems / 2];
             float fac[NT][2];  // of rows 2c and 2c + 1: what the scores are multiplied by
-            int limit[NT][2];  // dense: tokens that the row's position sees
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int row = row0 + nt * 8 + g;
@@ -123,12 +132,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                     for (int i = 0; i < kElems / 2; ++i) qf[nt][i] = flip ^ wds[i];
                 }
                 down = fmaxf(down, 1e-37f);  // a factor of 0 must not make NaN of an invisible token's -inf
-                const int sees = min(max(w.ctx - a.next_n + 1 + n, 0), w.ctx);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    fac[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
-                    limit[nt][j] = __shfl_sync(0xffffffffu, sees, 4 * (2 * c + j));
-                }
+                for (int j = 0; j < 2; ++j) fac[nt][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * c + j));
             }
 
             float o[NT][kTiles][4], sum[NT][4], m[NT][2], lraw[NT][2];
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                 ptx::cp_async_wait<S::kStages - 2>();
                 __syncwarp();
                 // which of the span's tokens rows 2c and 2c + 1 see
-                uint32_t sees[NT][2];
+                uint32_t sees[NT][2] = {};
                 bool all;
                 if constexpr (kList) {
                     const uint32_t s = __shfl_sync(0xffffffffu, loads.seen, stage);
@@ -157,13 +162,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
                     for (int nt = 0; nt < NT; ++nt) sees[nt][0] = sees[nt][1] = s;
                 } else {
                     all = t + kSpan <= min(w.t1, w.ctx - a.next_n + 1);
+                    if (!all) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int n = min(max(limit[nt][j] - t, 0), kSpan);
-                            sees[nt][j] = n == 32 ? 0xffffffffu : (1u << n) - 1;
-                        }
+                            for (int j = 0; j < 2; ++j) {
+                                const int draft = min((row0 + nt * 8 + 2 * c + j) / a.group, a.next_n - 1);
+                                const int limit = min(max(w.ctx - a.next_n + 1 + draft, 0), w.ctx);
+                                const int n = min(max(limit - t, 0), kSpan);
+                                sees[nt][j] = n == 32 ? 0xffffffffu : (1u << n) - 1;
+                            }
+                    }
                 }
                 loads.issue(a, ring + load_stage * S::kSlot, load_stage);
                 load_stage = load_stage + 1 == S::kStages ? 0 : load_stage + 1;
@@ -368,136 +377,158 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) attention_kernel(co
             next_row<kList>(a, r);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } while (pair < pairs_end && !kList);
+    } while (!last);
     if constexpr (!kList) {
         if (blockIdx.y == 0) dense_extras<D>(a, warp, kWarps, lane);
     }
 }
 
 // ---------------------------------------------------------------- combine
-// Joins the partial results of one query row: `wpr` warps a row, a lane takes
-// D / 32 elements of it.
+// Joins the partial results: `wpr` warps a query row, a lane takes D / 32 elements of
+// it. A CTA has `passes` times 8 / wpr rows of one item and kv head, after one look for
+// the ranges that hold their partials (178 rows with 71 query rows each, 2 kv heads,
+// two thirds of them split: 62 -> 57 us for the call against a look for every row).
 constexpr int kCombineThreads = 256;
+constexpr int64_t kCombineCtas = 148 * 8;
 
 template <int D, typename T, bool kList>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttentionArgs a, int wpr) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttentionArgs a, int wpr, int passes) {
     constexpr int kV = D / 32;  // elements of a lane
     __shared__ float part[8][D + 4];
     ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows_per_cta = 8 / wpr, sub = warp % wpr;
-    const int64_t id = (int64_t)blockIdx.x * rows_per_cta + warp / wpr;  // (item, hk, r)
+    const int hk = blockIdx.y % a.kv_heads;
+    const int item = blockIdx.x;
     const int64_t per_item = (int64_t)a.kv_heads * a.rows;
-    const int items = kList ? a.batch * a.next_n : a.batch;
-    const bool inside = id < items * per_item;
-    const int item = inside ? (int)(id / per_item) : 0;
-    const int hr = (int)(id - (int64_t)item * per_item);  // hk * rows + r
 
-    const int hk = hr / a.rows, r = hr - hk * a.rows;
-
-    // ranges first .. last (parts of the list) hold the row's partials
-    int first = 0, last = -1;
+    // ranges first .. last (parts of the list) hold the rows' partials
+    int first = 0, last = -1, parts = 0, first_cta = 0;
+    // the part that the head's range k begins at
+    auto range_start = [&](int k) {
+        if (a.kv_heads * parts <= a.num_ctas) return k;  // no CTA has two pairs
+        return k == 0 ? 0 : min(parts, first_pair(a, parts, first_cta + k) - hk * parts);
+    };
     if constexpr (kList) {
         last = a.splits - 1;
     } else {
         // the head's ranges that begin at or before the row's first token, and at or
         // before its last: warp-wide counts (they ascend)
         const int ctx = row_ctx(a, item);
+        if (ctx == 0) return;
+        parts = parts_with_rows(a, lane);
+        // the CTA that has the head's first pair: the last that begins at or before it
+        first_cta = parts == 0 ? 0 : (int)(((int64_t)(hk * parts + 1) * a.num_ctas - 1) / ((int64_t)a.kv_heads * parts));
         int at = 0, upto = 0;
         for (int k = lane;; k += 32) {
-            const int i = range_start(hk, k, a.kv_heads, a.num_ctas);
-            if (i >= a.num_ctas) break;
+            const int i = range_start(k);
+            if (i >= parts) break;
             const int b = __ldg(a.schedule + 2 * i), u = __ldg(a.schedule + 2 * i + 1);
             at += b < item || (b == item && u <= 0);
             upto += b < item || (b == item && (int64_t)u * kUnit < ctx);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            at += __shfl_xor_sync(0xffffffffu, at, o);
-            upto += __shfl_xor_sync(0xffffffffu, upto, o);
-        }
+        at = __reduce_add_sync(0xffffffffu, at);
+        upto = __reduce_add_sync(0xffffffffu, upto);
         first = max(at - 1, 0);
         last = upto - 1;
+        if (last <= first) return;
     }
-    bool work = inside;
-    if constexpr (!kList) work = work && last > first && row_ctx(a, item) > 0;
 
-    float top = kUnset, total = 0.f, raw = 0.f, v[kV] = {};
-    if (work) {
-        for (int i = first + sub; i <= last; i += wpr) {
-            const int64_t slot = kList ? (int64_t)item * a.splits + i
-                                       : 2 * (int64_t)range_start(hk, i, a.kv_heads, a.num_ctas) + (i == first);
-            const int64_t at = slot * per_item + hr;
-            const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + at * 4);
-            float p[kV];
-#pragma unroll
-            for (int k = 0; k < kV; ++k) p[k] = a.part_o[at * D + lane * kV + k];
-            const float to = fmaxf(top, ml.x);
-            const float keep = ex2(top - to), by = ex2(ml.x - to);
+    for (int pass = 0; pass < passes; ++pass) {
+        const int r = ((blockIdx.y / a.kv_heads) * passes + pass) * rows_per_cta + warp / wpr;
+        const int64_t hr = (int64_t)hk * a.rows + r;
+        float top = kUnset, total = 0.f, raw = 0.f, v[kV] = {};
+        auto join = [&](float m, float l, float l_raw, const float* p) {
+            const float to = fmaxf(top, m), keep = ex2(top - to), by = ex2(m - to);
             top = to;
-            total = total * keep + ml.y * by;
-            raw = raw * keep + ml.z * by;
+            total = total * keep + l * by;
+            raw = raw * keep + l_raw * by;
 #pragma unroll
             for (int k = 0; k < kV; ++k) v[k] = v[k] * keep + p[k] * by;
+        };
+        if (r < a.rows) {
+            for (int i = first + sub; i <= last; i += wpr) {
+                const int64_t slot = kList ? (int64_t)item * a.splits + i : 2 * (int64_t)range_start(i) + (i == first);
+                const int64_t at = slot * per_item + hr;
+                const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + at * 4);
+                float p[kV];
+#pragma unroll
+                for (int k = 0; k < kV; ++k) p[k] = a.part_o[at * D + lane * kV + k];
+                join(ml.x, ml.y, ml.z, p);
+            }
         }
+        if (wpr > 1) {
+            if (pass > 0) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kV; ++k) part[warp][lane * kV + k] = v[k];
+            if (lane == 0) {
+                part[warp][D] = top;
+                part[warp][D + 1] = total;
+                part[warp][D + 2] = raw;
+            }
+            __syncthreads();
+            if (sub != 0) continue;
+            for (int i = 1; i < wpr; ++i) {
+                const float* o = part[warp + i];
+                join(o[D], o[D + 1], o[D + 2], o + lane * kV);
+            }
+        }
+        if (r >= a.rows) continue;
+        const int n = kList ? item % a.next_n : r / a.group;
+        const int b = kList ? item / a.next_n : item;
+        const int64_t at = ((int64_t)b * a.next_n + n) * a.heads + hk * a.group + (kList ? r : r - n * a.group);
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * D + lane * kV);
+#pragma unroll
+        for (int k = 0; k < kV; k += 2) out[k / 2] = pack<T>(v[k] * inv, v[k + 1] * inv);
+        if (a.lse != nullptr && lane == 0) a.lse[at] = lse_of(top, raw);
     }
-    if (wpr > 1) {
-#pragma unroll
-        for (int k = 0; k < kV; ++k) part[warp][lane * kV + k] = v[k];
-        if (lane == 0) {
-            part[warp][D] = top;
-            part[warp][D + 1] = total;
-            part[warp][D + 2] = raw;
-        }
-        __syncthreads();
-        if (sub != 0) return;
-        for (int i = 1; i < wpr; ++i) {
-            const float* o = part[warp + i];
-            const float to = fmaxf(top, o[D]);
-            const float keep = ex2(top - to), by = ex2(o[D] - to);
-            top = to;
-            total = total * keep + o[D + 1] * by;
-            raw = raw * keep + o[D + 2] * by;
-#pragma unroll
-            for (int k = 0; k < kV; ++k) v[k] = v[k] * keep + o[lane * kV + k] * by;
-        }
-    }
-    if (!work) return;
-    const int n = kList ? item % a.next_n : r / a.group;
-    const int b = kList ? item / a.next_n : item;
-    const int64_t at = ((int64_t)b * a.next_n + n) * a.heads + hk * a.group + (kList ? r : r - n * a.group);
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + at * D + lane * kV);
-#pragma unroll
-    for (int k = 0; k < kV; k += 2) out[k / 2] = pack<T>(v[k] * inv, v[k + 1] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[at] = lse_of(top, raw);
 }
 
-template <int D, int NT, typename T, bool kList>
+template <int D, int NT, typename T, bool kList, bool kFew>
 cudaError_t launch_narrow(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    using S = Shape<D, NT>;
+    using S = Shape<D, NT, kFew>;
     static uint32_t done[64];
-    const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList>, device, S::kSmem, done);
+    const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList, kFew>, device, S::kSmem, done);
     if (e != cudaSuccess) return e;
     const int groups = (a.rows + S::kRows - 1) / S::kRows;
     const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
-    return launch_pdl(attention_kernel<D, NT, T, kList>, dim3((unsigned)x, groups), dim3(S::kThreads),
+    return launch_pdl(attention_kernel<D, NT, T, kList, kFew>, dim3((unsigned)x, groups), dim3(S::kThreads),
                       S::kSmem, stream, pdl, a);
+}
+
+// CTAs of 4 warps: where the list's part gives no more than 4 warps a span, or there are
+// enough lists to fill every SM with such CTAs (each then waits for its loads while the
+// others compute; 2192 lists of 43 tokens: 56 -> 15 us, 1024 of 1000: 67 -> 42 us, 600 of 512: 38 -> 20 us, 30 of 100: 4.9 -> 4.1 us).
+inline bool few_warps(const AttentionArgs& a) {
+    const int64_t ctas = (int64_t)a.batch * a.next_n * a.splits * a.kv_heads;
+    return a.topk <= 4 * kSpan || ctas >= 4 * 148;
 }
 
 template <int D, typename T, bool kList>
 cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    const cudaError_t e = a.rows <= 8    ? launch_narrow<D, 1, T, kList>(device, a, stream, pdl)
-                          : a.rows <= 16 ? launch_narrow<D, 2, T, kList>(device, a, stream, pdl)
-                                         : launch_wide<D, T, kList>(device, a, stream, pdl);
+    cudaError_t e;
+    if (a.rows > 16) {
+        e = launch_wide<D, T, kList>(device, a, stream, pdl);
+    } else if (kList && few_warps(a)) {
+        e = a.rows <= 8 ? launch_narrow<D, 1, T, true, true>(device, a, stream, pdl)
+                        : launch_narrow<D, 2, T, true, true>(device, a, stream, pdl);
+    } else {
+        e = a.rows <= 8 ? launch_narrow<D, 1, T, kList, false>(device, a, stream, pdl)
+                        : launch_narrow<D, 2, T, kList, false>(device, a, stream, pdl);
+    }
     if (e != cudaSuccess || (kList && a.splits == 1)) return e;
     const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
-    const int64_t parts = kList ? a.splits : (a.num_ctas + a.batch * a.kv_heads - 1) / (a.batch * a.kv_heads) + 1;
+    const int64_t pairs = items * a.kv_heads;
+    const int64_t parts = kList ? a.splits : (a.num_ctas + pairs - 1) / pairs + 1;
     int wpr = 1;
     while (wpr < 8 && wpr * 4 < parts) wpr *= 2;
-    const int64_t rows = items * a.kv_heads * a.rows;
-    return launch_pdl(combine_kernel<D, T, kList>, dim3((unsigned)((rows * wpr + 7) / 8)),
-                      dim3(kCombineThreads), 0, stream, pdl, a, wpr);
+    // as many CTAs as fit at once (8 to an SM), each with more rows where there are more
+    int64_t chunks = (a.rows * wpr + 7) / 8;
+    const int passes = (int)std::min(chunks, (pairs * chunks + kCombineCtas - 1) / kCombineCtas);
+    chunks = (chunks + passes - 1) / passes;
+    return launch_pdl(combine_kernel<D, T, kList>, dim3((unsigned)items, (unsigned)(a.kv_heads * chunks)),
+                      dim3(kCombineThreads), 0, stream, pdl, a, wpr, passes);
 }
 
 template <int D, typename T>

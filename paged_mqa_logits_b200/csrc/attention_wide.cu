@@ -245,8 +245,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
 
     ptx::griddep_wait();
 
-    int pair = blockIdx.x * a.kv_heads;  // dense: the next (head, part) pair
-    const int pairs_end = pair + a.kv_heads;
+    const int parts = kList ? 1 : parts_with_rows(a, lane);
+    int pair = kList ? 0 : first_pair(a, parts, blockIdx.x);  // dense: the next (head, part) pair
+    bool last = true;
     // Tiles so far: buffers and phases go by their number. Tile i is in S buffer i % 3,
     // for the i / 3-th time.
     int it = 0;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         const uint32_t tiles = base + (is_v ? W::kV : W::kK);
         uint64_t* const full = is_v ? bars->v_full : bars->k_full;
         do {
-            Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
+            Range r = open_range<kList>(a, blockIdx.x, parts, pair, last);
             SpanLoader<D, kTokens, kList, true> loads;
             loads.open(a, r, lane, dw * kSpan);
 #pragma unroll
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-        } while (ok && pair < pairs_end && !kList);
+        } while (ok && !last);
     } else if (warp <= kMmaWarp + 1) {
         // ------------------------------------------------------------ MMAs: the warp walks, lane 0 issues
         const bool is_s = warp == kMmaWarp;
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         const uint64_t v0 = ptx::smem_desc(base + W::kV, kTokens * 128, 1024, ptx::SW_128B);
         int seg = 0;
         do {
-            Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
+            Range r = open_range<kList>(a, blockIdx.x, parts, pair, last);
             while (ok && r.more) {
                 const int n = tiles_of(r.w);
                 if (is_s && n > 0) ok = wait_phase(&bars->q_full, seg++ & 1, bars, a.status, lane);
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 }
                 next_row<kList>(a, r);
             }
-        } while (ok && pair < pairs_end && !kList);
+        } while (ok && !last);
         // nothing of this CTA's MMAs is under way when it ends
         commit(lead, &bars->drain[is_s]);
         if (lane == 0) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         };
         const bool flip = a.scale_log2 < 0.f;  // a negative scale goes into q, so that the largest score is the largest S
         do {
-            Range r = open_range<kList>(a, blockIdx.x, pair, pairs_end);
+            Range r = open_range<kList>(a, blockIdx.x, parts, pair, last);
             while (ok && r.more) {
                 const Walk w = r.w;
                 const int n = tiles_of(w);
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 seg += n > 0;
                 next_row<kList>(a, r);
             }
-        } while (ok && pair < pairs_end && !kList);
+        } while (ok && !last);
     }
 
     if constexpr (!kList) {
