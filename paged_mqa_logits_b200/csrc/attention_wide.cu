@@ -37,6 +37,12 @@ constexpr int kDequantWarps = 4;   // for each of K and V
 constexpr int kMmaWarp = 0, kSoftmaxWarp = 4, kDequantWarp = kSoftmaxWarp + kSoftmaxWarps;
 constexpr int kWideThreads = 32 * (kDequantWarp + 2 * kDequantWarps);
 constexpr float kMost = 32768.f;
+// Registers of a thread: at launch (what the compiler gives 640 threads; the launch checks
+// it), and of the roles' four-warp groups afterwards, which together take no more, so that
+// the softmax groups' request is met once the others have given theirs back (32 rows of
+// two positions and 64 heads, 32768 to 131072 tokens: 227 -> 222 us).
+constexpr int kRegsLaunch = 96, kRegsMma = 48, kRegsSoftmax = 152, kRegsDequant = 64;
+static_assert(kRegsMma + 2 * kRegsSoftmax + 2 * kRegsDequant <= kWideThreads / 128 * kRegsLaunch, "registers");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 // TMEM columns: three S buffers of 128 (P over their second halves), O. With three, S
 // is two tiles ahead and no group waits for a product; Q is in shared memory for it.
@@ -77,6 +83,23 @@ struct Bars {
     uint32_t tmem;
 };
 static_assert(sizeof(Bars) <= 320, "barriers");
+
+// The warp's arrival: by the lane whose `lead` is 1, without a branch.
+__device__ __forceinline__ void arrive(uint32_t lead, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+        ::"r"(ptx::smem_u32(bar)), "r"(lead) : "memory");
+}
+
+// The whole four-warp group comes here.
+template <int kRegs>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (kRegs > kRegsLaunch)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // Waits for phase `parity`, by one thread. False: give up. A wait tells a phase from
 // the one before it, not from the one before that: who waits must know that the
@@ -253,7 +276,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
     int it = 0;
     bool ok = true;
 
+    if (warp < kSoftmaxWarp) set_registers<kRegsMma>();
     if (warp >= kDequantWarp) {
+        set_registers<kRegsDequant>();
         // ------------------------------------------------------------ dequantise
         const bool is_v = warp >= kDequantWarp + kDequantWarps;
         const int dw = (warp - kDequantWarp) & 3, row = dw * kSpan + lane;
@@ -285,7 +310,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     dequant_row<D>(slot, slot + kSpan * W::kRow, tiles + b * W::kBuf, lane, row);
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&full[b]);
+                    arrive(lane == 0, &full[b]);
                 }
                 next_row<kList>(a, r);
             }
@@ -352,6 +377,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         __syncwarp();
     } else if (warp >= kSoftmaxWarp) {
         // ------------------------------------------------------------ softmax
+        set_registers<kRegsSoftmax>();
         const int q4 = warp & 3, group = (warp - kSoftmaxWarp) >> 2;
         const int blocks = a.rows <= 32 ? 1 : a.rows <= 64 ? 2 : 4;  // of 32 rows; 4 / blocks copies of them
         const int place = q4 * 32 + lane;                 // of this thread in TMEM
@@ -364,7 +390,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         // a meeting of the group's warps
         auto meet = [&]() {
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->copies[group]);
+            arrive(lane == 0, &bars->copies[group]);
             return wait_phase(&bars->copies[group], meets++ & 1, bars, a.status, lane);
         };
         // the other group's value for this row
@@ -372,7 +398,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
             float* at = exch + (swaps & 1) * 256;
             at[group * 128 + place] = mine;
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->pair[q4]);
+            arrive(lane == 0, &bars->pair[q4]);
             const bool got = wait_phase(&bars->pair[q4], swaps & 1, bars, a.status, lane);
             other = at[(group ^ 1) * 128 + place];
             ++swaps;
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     fence_async_smem();
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->q_full);
+                    arrive(lane == 0, &bars->q_full);
                 }
                 fac = fmaxf(fac, 1e-37f);  // a factor of 0 must not make NaN of an invisible column's -inf
                 const int it0 = it;
@@ -583,12 +609,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                         }
                         if (j == 0 || had != m) ref[place] = m;
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&bars->turn[q4][b]);
+                        arrive(lane == 0, &bars->turn[q4][b]);
                         ptx::tmem_st_wait();
                         ptx::tc_fence_before();
                     }
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&bars->p_full[sb]);
+                    arrive(lane == 0, &bars->p_full[sb]);
                 }
                 it = it0 + n;
                 if (!ok) break;
@@ -722,6 +748,12 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
     static uint32_t done[64];
     const cudaError_t e = allow_smem(attention_wide_kernel<D, T, kList>, device, Wide<D>::kSmem, done);
     if (e != cudaSuccess) return e;
+    // a kernel launched with fewer registers would wait for them without end
+    static const int registers = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, attention_wide_kernel<D, T, kList>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if ((registers + 7) / 8 * 8 < kRegsLaunch) return cudaErrorInvalidConfiguration;
     const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
     return launch_pdl(attention_wide_kernel<D, T, kList>, dim3((unsigned)x), dim3(kWideThreads),
                       Wide<D>::kSmem, stream, pdl, a);
