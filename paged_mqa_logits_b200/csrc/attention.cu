@@ -21,12 +21,12 @@
 namespace mqa {
 namespace {
 
-// NT: query rows of a CTA / 8. More rows take more registers, so fewer warps. kFew: CTAs
-// of 4 warps, several to an SM, for short lists.
-template <int D, int NT, bool kFew>
+// NT: query rows of a CTA / 8. More rows take more registers, so fewer warps. kSmall: CTAs
+// of 4 warps, several to an SM, for token lists (see split_list).
+template <int D, int NT, bool kSmall>
 struct Shape {
-    static constexpr int kWarps = kFew ? 4 : NT == 1 ? 16 : 12;
-    static constexpr int kPerSm = kFew ? (NT == 1 ? 4 : 3) : 1;
+    static constexpr int kWarps = kSmall ? 4 : NT == 1 ? 16 : 12;
+    static constexpr int kPerSm = kSmall ? (NT == 1 ? 4 : 3) : 1;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRow = D / 2;                       // code bytes of a token
     static constexpr int kScales = D / 16;                   // scale bytes of a token
@@ -58,10 +58,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-template <int D, int NT, typename T, bool kList, bool kFew>
-__global__ void __launch_bounds__(Shape<D, NT, kFew>::kThreads, Shape<D, NT, kFew>::kPerSm)
+template <int D, int NT, typename T, bool kList, bool kSmall>
+__global__ void __launch_bounds__(Shape<D, NT, kSmall>::kThreads, Shape<D, NT, kSmall>::kPerSm)
 attention_kernel(const AttentionArgs a) {
-    using S = Shape<D, NT, kFew>;
+    using S = Shape<D, NT, kSmall>;
     constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
     constexpr int kTiles = D / 16;   // row tiles of O^T, and contraction steps of K Q^T
     constexpr int kElems = D / 4;    // elements of a row of q or K that one lane of a quad holds
@@ -485,24 +485,16 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     }
 }
 
-template <int D, int NT, typename T, bool kList, bool kFew>
+template <int D, int NT, typename T, bool kList, bool kSmall>
 cudaError_t launch_narrow(int device, const AttentionArgs& a, void* stream, bool pdl) {
-    using S = Shape<D, NT, kFew>;
+    using S = Shape<D, NT, kSmall>;
     static uint32_t done[64];
-    const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList, kFew>, device, S::kSmem, done);
+    const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList, kSmall>, device, S::kSmem, done);
     if (e != cudaSuccess) return e;
     const int groups = (a.rows + S::kRows - 1) / S::kRows;
     const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
-    return launch_pdl(attention_kernel<D, NT, T, kList, kFew>, dim3((unsigned)x, groups), dim3(S::kThreads),
+    return launch_pdl(attention_kernel<D, NT, T, kList, kSmall>, dim3((unsigned)x, groups), dim3(S::kThreads),
                       S::kSmem, stream, pdl, a);
-}
-
-// CTAs of 4 warps: where the list's part gives no more than 4 warps a span, or there are
-// enough lists to fill every SM with such CTAs (each then waits for its loads while the
-// others compute; 2192 lists of 43 tokens: 56 -> 15 us, 1024 of 1000: 67 -> 42 us, 600 of 512: 38 -> 20 us, 30 of 100: 4.9 -> 4.1 us).
-inline bool few_warps(const AttentionArgs& a) {
-    const int64_t ctas = (int64_t)a.batch * a.next_n * a.splits * a.kv_heads;
-    return a.topk <= 4 * kSpan || ctas >= 4 * 148;
 }
 
 template <int D, typename T, bool kList>
@@ -510,7 +502,7 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
     cudaError_t e;
     if (a.rows > 16) {
         e = launch_wide<D, T, kList>(device, a, stream, pdl);
-    } else if (kList && few_warps(a)) {
+    } else if (kList && a.small) {
         e = a.rows <= 8 ? launch_narrow<D, 1, T, true, true>(device, a, stream, pdl)
                         : launch_narrow<D, 2, T, true, true>(device, a, stream, pdl);
     } else {

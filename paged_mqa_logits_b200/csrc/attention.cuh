@@ -26,16 +26,26 @@ struct AttentionArgs {
     int32_t rows;             // query rows of one work item and kv head: group * next_n, or group (selected)
     int32_t page_size, ps_shift, num_pages, max_pages;
     int32_t num_ctas;         // dense: S
-    int32_t topk, splits;     // selected: list length, CTAs per list
+    int32_t topk, splits;     // selected: list length, CTAs per list,
+    bool small;               // of 4 warps
 };
 
-// CTAs that share one list of `topk` tokens: enough for a CTA on every SM, at most
-// one per 256 entries (8 of a CTA's warps, 32 tokens each).
-inline int topk_splits(int64_t lists, int topk, int sms) {
+// Selected: the CTAs that share one list of `topk` tokens, and if they are small (4
+// warps, several to an SM; up to 16 query rows a kv head). With more lists than SMs, one
+// small CTA a list: an SM then always has one that computes while others wait for their
+// loads (300 lists of 2048, D = 64: 40 -> 28 us, 256 of 1000: 21 -> 16 us, 2192 of 43:
+// 56 -> 15 us, against CTAs of 16 or 12 warps one after the other). With few lists, a
+// small CTA for every 128 tokens, if each can have an SM (8 lists of 2048: 8.2 -> 7.1
+// us). In between, large CTAs, one an SM, with 256 tokens or more (128 lists of 2048:
+// 21 us; 28 with 4 small ones).
+struct ListSplit { int splits; bool small; };
+inline ListSplit split_list(int64_t lists, int topk, int rows, int sms) {
+    if (rows <= 16 && lists > sms) return {1, true};
+    const int64_t small = (topk + 127) / 128, large = (topk + 255) / 256;
+    if (rows <= 16 && lists * small <= sms) return {(int)small, true};
     int64_t s = sms / (lists > 0 ? lists : 1);
-    const int64_t most = (topk + 255) / 256;
-    if (s > most) s = most;
-    return s < 1 ? 1 : (int)s;
+    if (s > large) s = large;
+    return {s < 1 ? 1 : (int)s, false};
 }
 
 // Slots of partial results: dense, two per part of the schedule (the row it
