@@ -146,6 +146,38 @@ def test_listed_tokens(case):
     Case(*shape, dtype, seed=40 + LISTS.index(case), k=k).run_and_check()
 
 
+def many(B, most, seed):
+    rng = np.random.default_rng(seed)
+    return [int(c) for c in rng.integers(0, most + 1, B)]
+
+
+MANY = [
+    # more (head, part) pairs than CTAs, in batches whose rows give fewer parts than CTAs; more rows than CTAs
+    (many(26, 7, 1), 2, 8, 8, 64, 16, "bf16", None, None),
+    (many(3, 900, 2), 1, 64, 64, 64, 16, "f16", None, None),
+    (many(20, 300, 3), 1, 144, 8, 128, 16, "bf16", None, None),
+    (many(9, 600, 4), 4, 120, 5, 64, 32, "bf16", 16, None),
+    (many(40, 30, 5), 1, 12, 12, 128, 64, "f16", 11, None),
+    (many(300, 40, 6), 1, 6, 2, 128, 16, "bf16", None, None),
+    (many(200, 300, 7), 1, 34, 2, 64, 16, "f16", None, None),
+    # lists: more than SMs (one CTA each), and fewer, of lengths for one large CTA or several
+    (many(40, 90, 8), 4, 12, 1, 128, 16, "bf16", None, 40),
+    (many(160, 300, 9), 1, 5, 1, 64, 32, "f16", None, 210),
+    (many(80, 300, 10), 2, 20, 2, 64, 16, "bf16", None, 130),
+    (many(40, 500, 11), 1, 16, 2, 128, 16, "bf16", None, 300),
+    (many(30, 900, 12), 1, 13, 1, 128, 64, "f16", None, 700),
+    (many(30, 900, 13), 1, 3, 1, 64, 64, "bf16", None, 700),
+    (many(20, 600, 14), 1, 10, 1, 64, 16, "f16", None, 500),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", MANY, ids=[f"{len(c[0])}-n{c[1]}-h{c[2]}.{c[3]}-d{c[4]}-s{c[7]}-k{c[8]}" for c in MANY])
+def test_many_rows_heads_and_lists(case):
+    *shape, dtype, ctas, k = case
+    Case(*shape, dtype, seed=70 + MANY.index(case), k=k).run_and_check(ctas)
+
+
 @gpu
 def test_lists_with_holes_repeats_and_tokens_out_of_sight():
     """-1 anywhere, tokens at and past the context, negatives, a token twice, and a
