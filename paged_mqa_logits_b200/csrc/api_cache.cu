@@ -99,7 +99,8 @@ int split_of(const mqa_attention_params* p, int device, AttentionArgs& a) {
     a.rows = p->topk > 0 ? a.group : a.group * p->next_n;
     a.num_ctas = p->num_ctas;
     a.topk = p->topk;
-    const ListSplit s = p->topk > 0 ? split_list((int64_t)p->batch * p->next_n * p->num_kv_heads, p->topk, a.rows, sms)
+    const ListSplit s = p->topk > 0 ? split_list((int64_t)p->batch * p->next_n * p->num_kv_heads, p->topk, a.rows,
+                                                 p->head_dim, sms)
                                     : ListSplit{1, false};
     a.splits = s.splits;
     a.small = s.small;

@@ -31,18 +31,25 @@ struct AttentionArgs {
 };
 
 // Selected: the CTAs that share one list of `topk` tokens, and if they are small (4
-// warps, several to an SM; up to 16 query rows a kv head). With more lists than SMs, one
-// small CTA a list: an SM then always has one that computes while others wait for their
-// loads (300 lists of 2048, D = 64: 40 -> 28 us, 256 of 1000: 21 -> 16 us, 2192 of 43:
-// 56 -> 15 us, against CTAs of 16 or 12 warps one after the other). With few lists, a
-// small CTA for every 128 tokens, if each can have an SM (8 lists of 2048: 8.2 -> 7.1
-// us). In between, large CTAs, one an SM, with 256 tokens or more (128 lists of 2048:
-// 21 us; 28 with 4 small ones).
+// warps, several to an SM; up to 16 query rows a kv head).
+// - More lists than SMs: one small CTA a list. An SM then always has one that computes
+//   while others wait for their loads (300 lists of 2048, D = 64: 40 -> 28 us, 256 of
+//   1000: 21 -> 16 us, 2192 of 43: 56 -> 15 us, against CTAs of 16 or 12 warps one after
+//   the other).
+// - Lists that one CTA does in a step or two are not split, which saves the joining
+//   and its launch (20 lists of 512: 15.7 -> 13.5 us a call, 6.8 -> 7.0 on the GPU; 45 of
+//   777, D = 64: 7.4 -> 6.5; but 16 of 1024, D = 128: 7.1 split, 9.2 whole).
+// - Few lists: a small CTA for every 128 tokens, if each can have an SM (8 lists of 2048:
+//   8.2 -> 7.1 us).
+// - In between, large CTAs, one an SM, with 256 tokens or more (128 lists of 2048: 21 us;
+//   28 with 4 small ones).
 struct ListSplit { int splits; bool small; };
-inline ListSplit split_list(int64_t lists, int topk, int rows, int sms) {
-    if (rows <= 16 && lists > sms) return {1, true};
+inline ListSplit split_list(int64_t lists, int topk, int rows, int head_dim, int sms) {
+    const bool narrow = rows <= 16;
+    if (narrow && (lists > sms || topk <= 128)) return {1, true};
+    if (topk <= (narrow && head_dim == 64 ? 1024 : 512)) return {1, false};
     const int64_t small = (topk + 127) / 128, large = (topk + 255) / 256;
-    if (rows <= 16 && lists * small <= sms) return {(int)small, true};
+    if (narrow && lists * small <= sms) return {(int)small, true};
     int64_t s = sms / (lists > 0 ? lists : 1);
     if (s > large) s = large;
     return {s < 1 ? 1 : (int)s, false};
