@@ -246,8 +246,16 @@ def paged_mqa_attention_fp4(q, k_cache, v_cache, block_table, context_lens, sche
     dev = q.get_device()
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if lse is None and with_lse:
-        lse = torch.empty(shape[:3], dtype=_FLOAT, device=q.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _shaped(out, shape, dev, q.dtype, "out")
+    if lse is not None:
+        lse_ptr = _shaped(lse, shape[:3], dev, _FLOAT, "lse")
+    elif with_lse:
+        lse = q.new_empty((B, next_n, H), dtype=_FLOAT)
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = None
     st = _ptr(status, dev, _INT, "status") or 0
     if scale is None:
         scale = D ** -0.5
@@ -262,8 +270,7 @@ def paged_mqa_attention_fp4(q, k_cache, v_cache, block_table, context_lens, sche
         q.data_ptr(), _ptr(k_cache, dev, _BYTE, "k_cache"), _ptr(v_cache, dev, _BYTE, "v_cache"),
         _ptr(block_table, dev, _INT, "block_table"),
         _sized(context_lens, B, dev, _INT, "context_lens"), _ptr(schedule, dev, _INT, "schedule"),
-        _ptr(indices, dev, _INT, "indices"), _shaped(out, shape, dev, q.dtype, "out"),
-        None if lse is None else _shaped(lse, shape[:3], dev, _FLOAT, "lse"),
+        _ptr(indices, dev, _INT, "indices"), out_ptr, lse_ptr,
         _ptr(workspace, dev, _BYTE, "workspace"), params(workspace.numel()), _stream(dev)))
     return out if lse is None else (out, lse)
 
