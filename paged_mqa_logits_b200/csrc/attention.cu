@@ -20,9 +20,9 @@
 // 2048 tokens, took 47 us here and 27 us there; one row of 1000 tokens 16.7 and 14.4.
 //
 // Measured: 64 rows of 1024 to 8192 tokens, 8 kv heads with 8 query heads each, D =
-// 128: 96 us for 342 MB, 3.6 TB/s or 0.55 of the copy rate. What bounds it is issue: 63
-// % of the issue slots, the integer pipe (e2m1 conversions, nibbles) at 56 %, the
-// tensor pipe at 22 %, and 14 % of the time before the first and after the last
+// 128: 88 us for 342 MB, 3.9 TB/s or 0.60 of the copy rate. What bounds it is issue: 63
+// % of the issue slots, the integer pipe (e2m1 conversions, nibbles) at 55 %, the
+// tensor pipe at 24 %, and 11 % of the time before the first and after the last
 // token. Rows of 16 query heads: 154 tokens a microsecond and SM, mma.sync at 0.7.
 #include <algorithm>
 
@@ -33,7 +33,7 @@ namespace mqa {
 namespace {
 
 // NT: query rows of a CTA / 8. More rows take more registers, so fewer warps. kSmall: CTAs
-// of 4 warps, several to an SM, for token lists (see split_list).
+// of 4 warps, several to an SM, for token lists (see split_list) and grouped heads (see launch_as).
 template <int D, int NT, bool kSmall>
 struct Shape {
     static constexpr int kWarps = kSmall ? 4 : NT == 1 ? 16 : 12;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
     int first = 0, last = -1, parts = 0, first_cta = 0;
     // the part that the head's range k begins at
     auto range_start = [&](int k) {
-        if (a.kv_heads * parts <= a.num_ctas) return k;  // no CTA has two pairs
+        if (a.kv_heads * parts <= a.deal) return k;  // no CTA has two pairs
         return k == 0 ? 0 : min(parts, first_pair(a, parts, first_cta + k) - hk * parts);
     };
     if constexpr (kList) {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Attentio
         if (ctx == 0) return;
         parts = parts_with_rows(a, lane);
         // the CTA that has the head's first pair: the last that begins at or before it
-        first_cta = parts == 0 ? 0 : (int)(((int64_t)(hk * parts + 1) * a.num_ctas - 1) / ((int64_t)a.kv_heads * parts));
+        first_cta = parts == 0 ? 0 : (int)(((int64_t)(hk * parts + 1) * a.deal - 1) / ((int64_t)a.kv_heads * parts));
         int at = 0, upto = 0;
         for (int k = lane;; k += 32) {
             const int i = range_start(k);
@@ -503,19 +503,29 @@ cudaError_t launch_narrow(int device, const AttentionArgs& a, void* stream, bool
     const cudaError_t e = allow_smem(attention_kernel<D, NT, T, kList, kSmall>, device, S::kSmem, done);
     if (e != cudaSuccess) return e;
     const int groups = (a.rows + S::kRows - 1) / S::kRows;
-    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
+    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.deal;
     return launch_pdl(attention_kernel<D, NT, T, kList, kSmall>, dim3((unsigned)x, groups), dim3(S::kThreads),
                       S::kSmem, stream, pdl, a);
 }
 
 template <int D, typename T, bool kList>
-cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl) {
+cudaError_t launch_as(int device, AttentionArgs a, void* stream, bool pdl) {
+    // Dense: with as many (head, part) pairs as small CTAs fit, those; rows begin and end
+    // in one CTA while the others compute (8 kv heads: 64 rows of 1024 to 8192 tokens 96 ->
+    // 88 us, 157 rows of 48 to 299 51 -> 26; 118 rows of one token, 4 kv heads, 22 -> 10;
+    // but 8 rows of 30000 to 60000, 8 kv heads, 96 -> 101).
+    a.deal = a.num_ctas;
+    if (!kList && a.rows <= 16) {
+        const int fit = 148 * (a.rows <= 8 ? Shape<D, 1, true>::kPerSm : Shape<D, 2, true>::kPerSm);
+        a.small = (int64_t)a.kv_heads * a.num_ctas >= fit;
+        if (a.small) a.deal = fit;
+    }
     cudaError_t e;
     if (a.rows > 16) {
         e = launch_wide<D, T, kList>(device, a, stream, pdl);
-    } else if (kList && a.small) {
-        e = a.rows <= 8 ? launch_narrow<D, 1, T, true, true>(device, a, stream, pdl)
-                        : launch_narrow<D, 2, T, true, true>(device, a, stream, pdl);
+    } else if (a.small) {
+        e = a.rows <= 8 ? launch_narrow<D, 1, T, kList, true>(device, a, stream, pdl)
+                        : launch_narrow<D, 2, T, kList, true>(device, a, stream, pdl);
     } else {
         e = a.rows <= 8 ? launch_narrow<D, 1, T, kList, false>(device, a, stream, pdl)
                         : launch_narrow<D, 2, T, kList, false>(device, a, stream, pdl);
@@ -523,7 +533,7 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
     if (e != cudaSuccess || (kList && a.splits == 1)) return e;
     const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
     const int64_t pairs = items * a.kv_heads;
-    const int64_t parts = kList ? a.splits : (a.num_ctas + pairs - 1) / pairs + 1;
+    const int64_t parts = kList ? a.splits : (a.deal + pairs - 1) / pairs + 1;
     int wpr = 1;
     while (wpr < 8 && wpr * 4 < parts) wpr *= 2;
     // as many CTAs as fit at once (8 to an SM), each with more rows where there are more

@@ -25,7 +25,8 @@ struct AttentionArgs {
     int32_t batch, next_n, heads, kv_heads, group;
     int32_t rows;             // query rows of one work item and kv head: group * next_n, or group (selected)
     int32_t page_size, ps_shift, num_pages, max_pages;
-    int32_t num_ctas;         // dense: S
+    int32_t num_ctas;         // dense: S, the parts of the schedule,
+    int32_t deal;             // and the CTAs that they are dealt to
     int32_t topk, splits;     // selected: list length, CTAs per list,
     bool small;               // of 4 warps
 };

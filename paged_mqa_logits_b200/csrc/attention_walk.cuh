@@ -163,11 +163,12 @@ __device__ __forceinline__ bool settle(const AttentionArgs& a, Walk& w, int u0) 
 // (head, part) pairs of the parts that have rows are dealt in order, evenly, over the
 // CTAs, so that a CTA walks neighbouring parts of one head as one range, rows are cut
 // S + Hk times over all heads at most, and batches with fewer rows than parts still
-// use every CTA (26 rows of at most 7 tokens, 8 kv heads: 25 -> 11 us).
+// use every CTA (26 rows of at most 7 tokens, 8 kv heads: 25 -> 11 us, 8 with small CTAs).
 // The first pair of CTA c, of `parts` parts that have rows.
 __device__ __forceinline__ int first_pair(const AttentionArgs& a, int parts, int c) {
-    if (parts == a.num_ctas) return c * a.kv_heads;
-    return (int)((int64_t)c * a.kv_heads * parts / a.num_ctas);
+    if (parts == a.deal) return c * a.kv_heads;
+    const uint64_t x = (uint64_t)((uint32_t)a.kv_heads * parts) * (uint32_t)c;
+    return (int)(x >> 32 ? x / (uint32_t)a.deal : (uint32_t)x / (uint32_t)a.deal);
 }
 
 // A warp's count of the parts that begin at a row of the batch: the first ones. One kv
@@ -263,9 +264,9 @@ __device__ __forceinline__ void dense_extras(const AttentionArgs& a, int warp, i
         ka.lib_status = a.status.lib;
         ka.batch = a.batch;
         ka.num_ctas = a.num_ctas;
-        check_schedule(ka, blockIdx.x, lane);
+        for (int i = blockIdx.x; i < a.num_ctas; i += gridDim.x) check_schedule(ka, i, lane);
     }
-    for (int b = blockIdx.x; b < a.batch; b += a.num_ctas) {
+    for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
         if (__ldg(a.context_lens + b) > 0) continue;
         const int64_t o = (int64_t)b * a.next_n * a.heads;
         for (int j = warp * 32 + lane; j < a.next_n * a.heads * (D / 8); j += warps * 32)

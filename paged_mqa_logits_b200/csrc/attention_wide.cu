@@ -764,7 +764,7 @@ cudaError_t launch_as(int device, const AttentionArgs& a, void* stream, bool pdl
         return cudaFuncGetAttributes(&at, attention_wide_kernel<D, T, kList>) == cudaSuccess ? at.numRegs : 0;
     }();
     if ((registers + 7) / 8 * 8 < kRegsLaunch) return cudaErrorInvalidConfiguration;
-    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.num_ctas;
+    const int64_t x = kList ? (int64_t)a.batch * a.next_n * a.splits * a.kv_heads : a.deal;
     return launch_pdl(attention_wide_kernel<D, T, kList>, dim3((unsigned)x), dim3(kWideThreads),
                       Wide<D>::kSmem, stream, pdl, a);
 }
