@@ -530,7 +530,9 @@ cudaError_t launch_as(int device, AttentionArgs a, void* stream, bool pdl) {
         e = a.rows <= 8 ? launch_narrow<D, 1, T, kList, false>(device, a, stream, pdl)
                         : launch_narrow<D, 2, T, kList, false>(device, a, stream, pdl);
     }
-    if (e != cudaSuccess || (kList && a.splits == 1)) return e;
+    // nothing to join: whole lists, or a table whose rows hold one unit of the schedule at
+    // most (4 rows of 22 to 200 tokens, 8 kv heads: 15.5 -> 13.4 us a call)
+    if (e != cudaSuccess || (kList ? a.splits == 1 : a.max_pages << a.ps_shift <= kUnit)) return e;
     const int64_t items = kList ? (int64_t)a.batch * a.next_n : a.batch;
     const int64_t pairs = items * a.kv_heads;
     const int64_t parts = kList ? a.splits : (a.deal + pairs - 1) / pairs + 1;
