@@ -14,7 +14,8 @@
 // warps join their (m, sum, O) through shared memory; rows that several CTAs share
 // leave partial results, which combine_kernel joins.
 //
-// For up to 16 query rows a kv head; beyond, attention_wide.cu. mma.sync runs one
+// For up to 16 query rows a kv head, and more with short lists (see split_list); beyond,
+// attention_wide.cu. mma.sync runs one
 // m16n8k16 every two cycles an SM, which 8 rows need 2.1 of a token (D = 128, K and V)
 // and 32 rows 8.5, against 6.3 cycles that HBM needs to bring it: 32 rows, lists of
 // 2048 tokens, took 47 us here and 27 us there; one row of 1000 tokens 16.7 and 14.4.
@@ -521,7 +522,7 @@ cudaError_t launch_as(int device, AttentionArgs a, void* stream, bool pdl) {
         if (a.small) a.deal = fit;
     }
     cudaError_t e;
-    if (a.rows > 16) {
+    if (a.rows > 16 && !(kList && a.small)) {
         e = launch_wide<D, T, kList>(device, a, stream, pdl);
     } else if (a.small) {
         e = a.rows <= 8 ? launch_narrow<D, 1, T, kList, true>(device, a, stream, pdl)

@@ -32,11 +32,15 @@ struct AttentionArgs {
 };
 
 // Selected: the CTAs that share one list of `topk` tokens, and if they are small (4
-// warps, several to an SM; up to 16 query rows a kv head).
+// warps and 8 or 16 query rows of a kv head, several to an SM).
 // - More lists than SMs: one small CTA a list. An SM then always has one that computes
 //   while others wait for their loads (300 lists of 2048, D = 64: 40 -> 28 us, 256 of
 //   1000: 21 -> 16 us, 2192 of 43: 56 -> 15 us, against CTAs of 16 or 12 warps one after
 //   the other).
+// - With more than 16 query rows a kv head, lists of up to 128 tokens, a small CTA for
+//   every 16 rows: each has one step to do, and the tile of attention_wide.cu only a
+//   chain of waits (480 lists of 7, 25 rows: 27 -> 10 us; 300 of 128, 64 rows: 28 -> 21;
+//   but 148 of 128, 128 rows: 11.5 there, 20 here).
 // - Lists that one CTA does in a step or two are not split, which saves the joining
 //   and its launch (20 lists of 512: 15.7 -> 13.5 us a call, 6.8 -> 7.0 on the GPU; 45 of
 //   777, D = 64: 7.4 -> 6.5; but 16 of 1024, D = 128: 7.1 split, 9.2 whole).
@@ -48,6 +52,7 @@ struct ListSplit { int splits; bool small; };
 inline ListSplit split_list(int64_t lists, int topk, int rows, int head_dim, int sms) {
     const bool narrow = rows <= 16;
     if (narrow && (lists > sms || topk <= 128)) return {1, true};
+    if (topk <= 128 && (rows <= 64 || lists * ((rows + 15) / 16) <= 3 * sms)) return {1, true};
     if (topk <= (narrow && head_dim == 64 ? 1024 : 512)) return {1, false};
     const int64_t small = (topk + 127) / 128, large = (topk + 255) / 256;
     if (narrow && lists * small <= sms) return {(int)small, true};

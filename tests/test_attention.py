@@ -168,6 +168,11 @@ MANY = [
     (many(30, 900, 12), 1, 13, 1, 128, 64, "f16", None, 700),
     (many(30, 900, 13), 1, 3, 1, 64, 64, "bf16", None, 700),
     (many(20, 600, 14), 1, 10, 1, 64, 16, "f16", None, 500),
+    # short lists of more than 16 query rows
+    (many(50, 300, 15), 4, 75, 3, 64, 16, "bf16", None, 7),
+    (many(3, 300, 16), 1, 112, 1, 128, 32, "f16", None, 100),
+    (many(160, 300, 17), 1, 33, 1, 128, 16, "bf16", None, 128),
+    (many(150, 200, 18), 1, 100, 1, 64, 64, "bf16", None, 60),
 ]
 
 
