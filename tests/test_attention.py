@@ -173,6 +173,11 @@ MANY = [
     (many(3, 300, 16), 1, 112, 1, 128, 32, "f16", None, 100),
     (many(160, 300, 17), 1, 33, 1, 128, 16, "bf16", None, 128),
     (many(150, 200, 18), 1, 100, 1, 64, 64, "bf16", None, 60),
+    # tables that hold one unit of the schedule a row
+    (many(30, 112, 19), 2, 57, 3, 64, 16, "bf16", None, None),
+    (many(170, 96, 20), 1, 33, 1, 128, 32, "f16", None, None),
+    (many(9, 64, 21), 4, 4, 1, 128, 64, "bf16", 3, None),
+    (many(12, 192, 22), 3, 62, 2, 64, 64, "f16", 30, None),
 ]
 
 
