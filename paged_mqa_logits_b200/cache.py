@@ -91,12 +91,16 @@ def _check(rc: int) -> None:
         check(rc)
 
 
+# of the current device, without torch.cuda's own check that CUDA is set up (a CUDA tensor is there)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _elsewhere(t: torch.Tensor, stream) -> bool:
     """Whether a call on t's device and `stream` needs the current ones changed."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    return stream is not None or dev != torch.cuda.current_device()
+    return stream is not None or dev != _current()
 
 
 @contextlib.contextmanager
