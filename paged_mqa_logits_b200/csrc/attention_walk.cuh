@@ -162,13 +162,12 @@ __device__ __forceinline__ bool settle(const AttentionArgs& a, Walk& w, int u0) 
 // The parts of the schedule that the CTAs of a dense launch take: with Hk kv heads the
 // (head, part) pairs of the parts that have rows are dealt in order, evenly, over the
 // CTAs, so that a CTA walks neighbouring parts of one head as one range, rows are cut
-// S + Hk times over all heads at most, and batches with fewer rows than parts still
-// use every CTA (26 rows of at most 7 tokens, 8 kv heads: 25 -> 11 us, 8 with small CTAs).
+// once a CTA and head at most, and batches with fewer rows than parts still use every
+// CTA (26 rows of at most 7 tokens, 8 kv heads: 25 -> 11 us, 8 with small CTAs).
 // The first pair of CTA c, of `parts` parts that have rows.
 __device__ __forceinline__ int first_pair(const AttentionArgs& a, int parts, int c) {
     if (parts == a.deal) return c * a.kv_heads;
-    const uint64_t x = (uint64_t)((uint32_t)a.kv_heads * parts) * (uint32_t)c;
-    return (int)(x >> 32 ? x / (uint32_t)a.deal : (uint32_t)x / (uint32_t)a.deal);
+    return (int)((int64_t)c * a.kv_heads * parts / a.deal);
 }
 
 // A warp's count of the parts that begin at a row of the batch: the first ones. One kv
