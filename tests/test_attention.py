@@ -350,6 +350,31 @@ def test_captured_replayed_and_on_another_stream(k):
 
 
 @gpu
+def test_calls_on_several_streams_at_once():
+    """Every kernel (wide, narrow, small CTAs, joined and not) on a stream and with a
+    workspace of its own, all under way together: the bytes of the calls one by one."""
+    shapes = [(([900, 30, 700], 2, 64, 1, 128, 64), None), (([500] * 9, 1, 48, 8, 64, 16), None),
+              (([800, 300], 1, 12, 1, 128, 32), None), ((many(200, 200, 3), 1, 8, 1, 64, 16), 150),
+              (([600] * 4, 1, 8, 1, 128, 64), 2048)]
+    runs = []
+    for i, (shape, k) in enumerate(shapes):
+        c = Case(*shape, seed=120 + i, k=k)
+        d = c.gpu()
+        work = mq.mqa_attention_workspace(d["q"], kv_heads=c.Hk, topk=k or 0)
+        runs.append((c, d, work, torch.cuda.Stream(), c.call(d, workspace=work, with_lse=True)))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for c, d, work, stream, _ in runs:
+            with torch.cuda.stream(stream):
+                got.append(c.call(d, workspace=work, with_lse=True))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        want = runs[i % len(runs)][4]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@gpu
 def test_pages_behind_four_gigabytes():
     """Byte offsets past 2^32 in a pool of 9 million pages."""
     c = Case([200, 90], 1, 8, 1, 64, 16, seed=80)
