@@ -303,6 +303,22 @@ def test_stale_schedule_is_reported():
 
 
 @gpu
+@pytest.mark.parametrize("heads,ctas", [(8, None), (64, None), (1, 600), (5, 3)])
+def test_validation_with_more_and_fewer_ctas_than_parts(heads, ctas):
+    c = Case([600, 0, 300], 2, heads, heads, 64, 16, seed=68)
+    d = c.gpu()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for lens, stale in ((c.ctx, 0), (torch.tensor([600, 0, 10], dtype=torch.int32), mq.MQA_STATUS_STALE_SCHEDULE)):
+        sched = mq.mqa_logits_schedule(lens.cuda(), ctas)
+        out = mq.paged_mqa_attention_fp4(d["q"], d["k"], d["v"], d["table"], d["ctx"], sched, page_size=16,
+                                         kv_heads=heads, scale=c.scale, flags=mq.MQA_FLAG_VALIDATE, status=status)
+        assert int(status) == stale
+        if not stale:
+            c.check(out)
+    mq.mqa_logits_clear_status()
+
+
+@gpu
 @pytest.mark.parametrize("k", [None, 600], ids=["all", "list"])
 def test_captured_replayed_and_on_another_stream(k):
     """A replay follows new lengths, queries and cache contents; two graphs with a
