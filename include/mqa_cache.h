@@ -117,8 +117,9 @@ typedef struct mqa_append_params {
  * b's tokens are i = row_offsets[b] .. row_offsets[b+1]-1, and the last of them
  * becomes position context_lens[b] - 1 (context_lens counts the new tokens
  * already, as the logits and attention calls that follow expect). With
- * row_offsets NULL every row has T / B tokens (T a multiple of B). Tokens at or
- * behind row_offsets[B] (a padded batch) are not looked at. A token whose
+ * row_offsets NULL every row has T / B tokens (T a multiple of B). Tokens before
+ * row_offsets[0] and at or behind row_offsets[B] (a slice of a batch's offsets, a
+ * padded batch) belong to no row and are not written. A token whose
  * position is negative, behind the block table or on a page outside
  * [0, num_pages) is not written (validate mode: MQA_STATUS_BAD_CONTEXT /
  * _BAD_PAGE). Other slots keep their bytes. Two tokens must not have the same

@@ -103,13 +103,13 @@ struct Place {
 __device__ __forceinline__ Place place_of(const AppendArgs& a, int t) {
     int b, left;  // left: the tokens of the row from t on
     if (a.row_offsets != nullptr) {
-        int lo = 0, hi = a.batch;  // the last row that begins at or before t
+        int lo = -1, hi = a.batch;  // the last row that begins at or before t (-1: none does)
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (__ldg(a.row_offsets + mid) <= t) lo = mid; else hi = mid - 1;
         }
         b = lo;
-        if (b >= a.batch) return {-1, 0};
+        if (b < 0 || b >= a.batch) return {-1, 0};
         left = __ldg(a.row_offsets + b + 1) - t;
         if (left <= 0) return {-1, 0};
     } else {

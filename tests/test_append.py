@@ -151,6 +151,36 @@ def test_fp8(case, small):
 
 
 @gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_a_slice_of_the_offsets(fp8, first):
+    """Some of a batch's rows, with their part of the offsets and the whole batch's tokens: those
+    before the first row and behind the last have no row, and what is cached stays."""
+    new, ctx, ps, D = [3, 5, 0, 2, 4], [40, 10, 7, 33, 4], 16, 64
+    table, P = setup(ctx, ps, seed=3)
+    offsets = [0, *np.cumsum(new).tolist()]
+    off, table, ctx = offsets[first:5], table[first:4].contiguous(), ctx[first:4]
+    T = offsets[-1]
+    x = tokens((T, 1, D), torch.bfloat16, seed=12)
+    g = torch.Generator().manual_seed(13)
+    cache = torch.randint(0, 256, (P, ps * (D + 4) if fp8 else ps * 36), generator=g, dtype=torch.uint8)
+    where = places(table, ctx, off, T, ps, P)
+    assert where[:off[0]] == [None] * off[0] and where[-4:] == [None] * 4
+    dc, values = cache.cuda(), torch.full((T, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    args = [torch.as_tensor(a, dtype=torch.int32).cuda() for a in (table, ctx, off)]
+    if fp8:
+        mq.mqa_cache_append_fp8(x[:, 0].cuda(), dc, *args, page_size=ps, values=values[:, 0])
+        want, vals = expected_fp8(cache.numpy(), x[:, 0], where, ps)
+    else:
+        mq.mqa_cache_append_fp4(x.cuda(), None, dc, None, *args, page_size=ps, k_values=values)
+        want, vals = expected_fp4(cache.numpy(), x, where, 1, ps)
+    np.testing.assert_array_equal(dc.cpu().numpy(), want)
+    for t in range(T):
+        w = torch.from_numpy(vals[t]).to(torch.bfloat16).view(D) if where[t] else torch.full((D,), 7.0).to(torch.bfloat16)
+        assert torch.equal(values[t, 0].cpu(), w), t
+
+
+@gpu
 def test_even_rows_strides_and_keys_alone():
     """No offsets: T / B tokens a row; a strided slice of a projection; an FP4 cache
     of keys without values."""
