@@ -111,7 +111,9 @@ def _there(t: torch.Tensor, stream):
             yield
             return
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+            # handle 0 is the default stream; ExternalStream takes it for none given and makes a new one
+            stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+                      else torch.cuda.default_stream(t.device))
         if stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.stream(stream):

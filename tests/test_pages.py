@@ -237,6 +237,29 @@ def test_unaligned_counts_and_a_captured_step():
         np.testing.assert_array_equal(cache.cpu().numpy(), cells)
 
 
+@gpu
+def test_streams_by_object_and_by_handle(monkeypatch):
+    """The stream that the library is given: raw handles, 0 (the default stream) among
+    them, streams, and the current one."""
+    from paged_mqa_logits_b200 import cache as binding
+    used, lib = [], mq.library()
+
+    class Spy:
+        @staticmethod
+        def mqa_pages_copy(*args):
+            used.append(args[-1])
+            return lib.mqa_pages_copy(*args)
+
+    monkeypatch.setattr(binding, "_library", Spy)
+    pages = torch.zeros(4, 64, dtype=torch.uint8, device="cuda")
+    src, dst = dev([0], [1])
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for stream in (0, side.cuda_stream, torch.cuda.default_stream(), side, None):
+            mq.mqa_pages_copy(pages, src, dst, stream=stream)
+    assert used == [0, side.cuda_stream, 0, side.cuda_stream, side.cuda_stream]
+
+
 # ---------------------------------------------------------------- refusals (CPU)
 def params(**kw):
     base = dict(batch=2, out_batch=2, max_pages_per_row=4, num_pages=8, page_size=16, flags=0, status=None)
