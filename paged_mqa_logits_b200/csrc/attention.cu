@@ -3,7 +3,8 @@
 // The mathematics: o = sum_t p_t v_t / sum_t p_t with p_t = 2^(x_t - m), x_t the
 // score in base 2 and m a running reference of the row that is at most its
 // maximum. m is raised (and what was summed so far rescaled) only when a score
-// exceeds it by kSlack, so p <= 2^kSlack fits f16 and most tiles need no rescale.
+// exceeds it by kSlack, to kRoom below the maximum, so p fits f16, few of the small
+// ones vanish, and most tiles need no rescale.
 //
 // One warp takes 32 tokens at a time through its own ring of asynchronous copies
 // (no CTA barrier inside a row) and dequantises K and V straight into the A
@@ -261,7 +262,7 @@ attention_kernel(const AttentionArgs a) {
 #pragma unroll
                                 for (int d = 4; d < 32; d <<= 1)
                                     to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
-                                to = fmaxf(to, m[nt][j]);
+                                to = fmaxf(to - kRoom, m[nt][j]);
                                 const float by = ex2(m[nt][j] - to);
                                 m[nt][j] = to;
 #pragma unroll

@@ -9,7 +9,16 @@ namespace mqa {
 
 constexpr int kSpan = 32;         // tokens of a ring slot
 constexpr float kUnset = -1e30f;  // m of a row that has seen no token
-constexpr float kSlack = 15.f;    // p <= 2^15, within f16; the largest p is at least 1
+// p = 2^(x - m) is rounded to f16 for the second product: 11 bits down to 2^-14, an
+// absolute 2^-25 below. That is off by 2^-11 of each p at most, either way, which in the
+// result is less than its own rounding to bf16 and about as much as that to f16; p in two
+// f16 parts would double the second product. m is raised when an x exceeds it by kSlack (p
+// stays below f16's 65504), and then to kRoom below the row's maximum: the largest p is at
+// least 2^kRoom, so that a p keeps its 11 bits down to 2^-21 of the largest, and 2^17 tokens
+// whose p vanish (2^-32 of it each) held at most 2^-15 of the row. With m raised to the maximum
+// itself that was 2^-8 (and 1 to 4 % less time: 32 rows of two positions and 64 heads, 32768 to
+// 131072 tokens, 239 us for 241 to 249; 128 lists of 2048, 32 heads, 28.1 for 28.8).
+constexpr float kSlack = 15.99f, kRoom = 7.f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

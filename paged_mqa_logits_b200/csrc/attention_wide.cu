@@ -18,7 +18,8 @@
 // have two buffers of f16, S three.
 //
 // m is raised, by whole numbers so that every rescaling is exact, only when the p of
-// 32 tokens sum to more than kMost (so that none is outside f16). A tile is computed with the m that its
+// 32 tokens sum to more than kMost (so that none is outside f16), and then to kRoom
+// below the largest score. A tile is computed with the m that its
 // group knows; at its end the group learns the m that O has by then (`ref`, settled
 // in turn, tile by tile) and scales whichever of P and O is behind, which is rare. So
 // a tile needs one pass over S, and the groups wait for each other only where one
@@ -46,7 +47,7 @@ constexpr int kDequantWarps = 4;   // for each of K and V
 // in their quarters of TMEM), then the softmax and the dequantising warps.
 constexpr int kMmaWarp = 0, kSoftmaxWarp = 4, kDequantWarp = kSoftmaxWarp + kSoftmaxWarps;
 constexpr int kWideThreads = 32 * (kDequantWarp + 2 * kDequantWarps);
-constexpr float kMost = 32768.f;
+constexpr float kMost = 65504.f;
 // Registers of a thread: at launch (what the compiler gives 640 threads; the launch checks
 // it), and of the roles' four-warp groups afterwards, which together take no more, so that
 // the softmax groups' request is met once the others have given theirs back (32 rows of
@@ -472,7 +473,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                 fac = fmaxf(fac, 1e-37f);  // a factor of 0 must not make NaN of an invisible column's -inf
                 const int it0 = it;
                 const uint64_t fac2 = ptx::f32x2_pack(fac, fac);
-                uint64_t l2 = 0;  // two partial sums of p, relative to m
+                // two partial sums of p, relative to m, before its rounding to f16: the lse needs
+                // those, and for the result the roundings, 2^-11 of each p either way, matter no
+                // less in the products than in the sum
+                uint64_t l2 = 0;
                 auto scale_l = [&](float by) {
                     float l0, l1;
                     ptx::f32x2_unpack(l2, l0, l1);
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                                 }
                                 // every row of the warp goes along, to what it sees here: the
                                 // rescaling costs the warp the same, and the next one comes later
-                                const float to = fmaxf(m, floorf(max3(max3(most[0], s[30], s[31]), most[1], most[1]) * fac));
+                                const float to = fmaxf(m, floorf(max3(max3(most[0], s[30], s[31]), most[1], most[1]) * fac) - kRoom);
                                 scale_l(ex2(m - to));
 #pragma unroll 1
                                 for (int k = chunk1 - 1; k > i; --k) scale_p(p_at + 16 * k, m - to);

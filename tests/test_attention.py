@@ -231,6 +231,44 @@ def test_scores_that_rise_along_the_row():
 
 
 @gpu
+@pytest.mark.parametrize("at", [0, 20000])
+@pytest.mark.parametrize("heads", [8, 12, 32, 64, 128])
+@pytest.mark.parametrize("listed", [False, True])
+def test_a_sink_over_a_long_flat_row(listed, heads, at):
+    """One token 17.5 nats above all others, whose v is 0: the result is what the others
+    hold, 0.0034 (lists: 0.0009) of the mass, each p below 2^-25 of the largest. One CTA has
+    the whole row."""
+    T, D, ps, rows = (32768, 128, 64, 160) if listed else (131072, 128, 64, 1)
+    c = Case([1], 1, heads, 1, D, ps)
+    g = torch.Generator().manual_seed(96)
+    q = 1 + torch.arange(heads) % 3 / 128
+    c.q = q.to(torch.bfloat16)[None, None, :, None].expand(rows, 1, heads, D)
+    c.scale = 17.5 / D
+    c.k, c.v = (torch.zeros(T // ps, ps * (D // 2 + D // 16), dtype=torch.uint8) for _ in range(2))
+    order = torch.randperm(T // ps, generator=g).to(torch.int32)
+    c.table, c.ctx = order.expand(rows, -1).contiguous(), torch.full((rows,), T, dtype=torch.int32)
+    page, slot = int(order[at // ps]), at % ps
+    for pool in (c.k, c.v):
+        codes, scales = c.split(pool)
+        scales.fill_(0x38)  # 1
+        if pool is c.v:
+            codes.copy_(torch.randint(2, 5, codes.shape, generator=g) * 17)  # 1 to 2
+        codes[page, 0, slot] = 0x22 if pool is c.k else 0  # every element 1 against 0; 0
+    if listed:
+        c.indices = torch.arange(T, dtype=torch.int32).expand(rows, 1, T).contiguous()
+    got, lse = c.call(c.gpu(), 1, with_lse=True)
+    assert torch.equal(got, got[:1].expand_as(got)) and torch.equal(lse, lse[:1].expand_as(lse))
+    total = T - 1 + np.exp(17.5 * q.double().numpy())[:, None]
+    o = ref.decode_fp4(c.v.numpy(), 1, ps, D).sum((0, 1, 2)) / total
+    # the roundings of ref.check_attention, but an absolute one of p (three of them where P is
+    # rescaled) is 2^-25 where the largest p is 2^7 at least, and moves o by |v - o| <= 2 of it
+    err = 18 * 2.0 ** -16
+    bound = 2.0 ** -8 * o + 2 * (err + 2.0 ** -11 + 2.0 ** -19) * o + T * 3 * 2.0 ** -32 * 2
+    assert (np.abs(got[0, 0].double().cpu().numpy() - o) <= bound).all()
+    assert (np.abs(lse[0, 0].double().cpu().numpy() - np.log(total[:, 0])) <= err + (T + 64) * 2.0 ** -24 + 2.0 ** -15).all()
+
+
+@gpu
 @pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
 def test_scales(scale):
     c = Case([290, 31], 2, 6, 2, 64, 32, "f16", seed=63, q_gain=0.5)
