@@ -185,6 +185,26 @@ attention_kernel(const AttentionArgs a) {
                                 const int n = min(max(limit - t, 0), kSpan);
                                 sees[nt][j] = n == 32 ? 0xffffffffu : (1u << n) - 1;
                             }
+                        if (a.next_n > 1) {
+                            // tokens that not every position sees: see nan_bytes. This lane's elements of O
+                            // are all in one block of 16.
+                            uint32_t nan = 0;
+                            if (t + lane > w.ctx - a.next_n)
+                                nan = clear_nan<D>(ring + stage * S::kSlot + kSpan * (2 * S::kRow + S::kScales) + lane * S::kScales);
+                            for (uint32_t left = __ballot_sync(0xffffffffu, nan != 0); left; left &= left - 1) {
+                                const int from = __ffs(left) - 1;
+                                const uint32_t bits = __shfl_sync(0xffffffffu, nan, from);
+                                if (!((bits >> (D == 128 ? g : g / 2)) & 1)) continue;
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j)
+                                        if ((sees[nt][j] >> from) & 1)
+#pragma unroll
+                                            for (int i = 0; i < kTiles; ++i) o[nt][i][j] = o[nt][i][j + 2] = kNan;
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
                 loads.issue(a, ring + load_stage * S::kSlot, load_stage);

@@ -75,7 +75,7 @@ struct Wide {
     static constexpr int kRef = kExch + 2 * 2 * 128 * 4;                       // [128] fp32: m of each row
     static constexpr int kTot = kRef + 128 * 4;                                // [2][128] fp32: sums of p
     static constexpr int kBars = kTot + 2 * 128 * 4;
-    static constexpr int kSmem = kBars + 320 + 1024;  // slack for aligning the base
+    static constexpr int kSmem = kBars + 384 + 1024;  // slack for aligning the base
     static_assert(kSmem <= 232448, "more shared memory than a CTA can have");
 };
 
@@ -90,10 +90,13 @@ struct Bars {
     uint64_t pair[4];               // the two warps of a row quarter exchange values
     uint64_t copies[2];             // a group's warps: at the row's end, where rows stand in copies
     uint64_t drain[2];
+    // the NaN scales of V in the tokens that not every position of a row sees (nan_bytes), by
+    // the row's number modulo 4: written by the warps that dequantise V, read at the row's end
+    uint32_t nan[4][4];
     int32_t abort;
     uint32_t tmem;
 };
-static_assert(sizeof(Bars) <= 320, "barriers");
+static_assert(sizeof(Bars) <= 384, "barriers");
 
 // The warp's arrival: by the lane whose `lead` is 1, without a branch.
 __device__ __forceinline__ void arrive(uint32_t lead, uint64_t* bar) {
@@ -296,6 +299,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
         const uint32_t ring = base + W::kRing + (warp - kDequantWarp) * (W::kStages * W::kSlot);
         const uint32_t tiles = base + (is_v ? W::kV : W::kK);
         uint64_t* const full = is_v ? bars->v_full : bars->k_full;
+        uint32_t seg = 0;
         do {
             Range r = open_range<kList>(a, blockIdx.x, parts, pair, last);
             SpanLoader<D, kTokens, kList, true> loads;
@@ -318,11 +322,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                                   : wait_phase(&bars->s_full[(it - 2) % kBufS], (it - 2) / kBufS & 1, bars, a.status, lane);
                     }
                     if (!ok) break;
+                    if constexpr (!kList) {
+                        if (is_v && a.next_n > 1) {  // this lane's token: the i-th of those that not every position sees?
+                            const int i = r.w.t0 + j * kTokens + row - (r.w.ctx - a.next_n + 1);
+                            if (i >= 0 && i < a.next_n - 1)
+                                bars->nan[seg & 3][i] = clear_nan<D>(slot + kSpan * W::kRow + lane * W::kScales);
+                        }
+                    }
                     dequant_row<D>(slot, slot + kSpan * W::kRow, tiles + b * W::kBuf, lane, row);
                     fence_async_smem();
                     __syncwarp();
                     arrive(lane == 0, &full[b]);
                 }
+                ++seg;
                 next_row<kList>(a, r);
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
@@ -668,6 +680,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                         by = ex2(m - top);
                         m = top;
                     }
+                    // Written before the last tile's v_full, which its products and so the wait above
+                    // are behind; and a row four on is dequantised only after the products of the
+                    // row before last, for which both groups have left this one.
+                    uint32_t nan = 0;  // in tokens that this position sees
+                    if constexpr (!kList) {
+#pragma unroll 1
+                        for (int i = 0; i < draft; ++i) {
+                            const int t = w.ctx - a.next_n + 1 + i;
+                            if (t >= w.t0 && t < w.t1) nan |= bars->nan[seg & 3][i];
+                        }
+                    }
                     int64_t slot;
                     const bool whole = row_is_whole<kList>(a, r, slot);
                     const int64_t at_part = (slot * a.kv_heads + r.hk) * a.rows + row;
@@ -675,14 +698,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) attention_wide_kernel(const A
                     // 8 elements of the row's result, from element d on
                     auto put = [&](int d, const float* o) {
                         if (row >= a.rows) return;
+                        const float f = (nan >> (d >> 4)) & 1 ? kNan : whole ? inv : 1.f;
                         if (whole) {
                             *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + at_row * D + d) =
-                                make_uint4(pack<T>(o[0] * inv, o[1] * inv), pack<T>(o[2] * inv, o[3] * inv),
-                                           pack<T>(o[4] * inv, o[5] * inv), pack<T>(o[6] * inv, o[7] * inv));
+                                make_uint4(pack<T>(o[0] * f, o[1] * f), pack<T>(o[2] * f, o[3] * f),
+                                           pack<T>(o[4] * f, o[5] * f), pack<T>(o[6] * f, o[7] * f));
                         } else {
                             float4* out = reinterpret_cast<float4*>(a.part_o + at_part * D + d);
-                            out[0] = make_float4(o[0], o[1], o[2], o[3]);
-                            out[1] = make_float4(o[4], o[5], o[6], o[7]);
+                            out[0] = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+                            out[1] = make_float4(o[4] * f, o[5] * f, o[6] * f, o[7] * f);
                         }
                     };
                     if (n == 0 || blocks == 4) {

@@ -276,6 +276,52 @@ def test_scales(scale):
     c.run_and_check()
 
 
+NAN = [
+    # the last tokens across the ends of spans, tiles, units of the schedule and pages
+    ([257, 5, 1, 70], 2, 4, 1, 128, 16, "bf16", None),
+    ([257, 514, 3], 3, 4, 2, 64, 32, "f16", 2),
+    ([258, 33, 34], 4, 3, 1, 128, 16, "bf16", 148),
+    ([64, 33, 34, 1, 2, 3], 2, 5, 5, 64, 32, "bf16", None),
+    ([257, 100], 2, 16, 1, 128, 64, "bf16", None),
+    ([257, 129, 2], 4, 16, 2, 128, 64, "f16", None),
+    ([257, 600, 129, 3], 3, 20, 1, 64, 16, "bf16", 3),
+    ([258, 514, 2], 4, 32, 1, 128, 64, "bf16", 2),
+    ([130, 0, 257], 2, 40, 2, 64, 64, "f16", 1),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", NAN, ids=[f"{c[0][0]}-n{c[1]}-h{c[2]}.{c[3]}-d{c[4]}-{c[6]}" for c in NAN])
+def test_nan_that_later_positions_see(case):
+    """NaN scales of V in a row's last tokens reach the blocks of 16 elements, and the
+    positions, that see them, and no others."""
+    *shape, dtype, ctas = case
+    c = Case(*shape, dtype, seed=90 + NAN.index(case))
+    clean, nn, D, ps = c.v.clone(), c.nn, c.D, c.ps
+    nan = torch.zeros(len(c.ctx), nn, c.H, D, dtype=torch.bool)
+    g = torch.Generator().manual_seed(3)
+    codes, scales = c.split(c.v)
+    _, safe = Case.split(c, clean)
+    for b, ctx in enumerate(c.ctx.tolist()):
+        for t in range(max(ctx - nn + 1, 0), ctx):
+            page, s = int(c.table[b, t // ps]), t % ps
+            for h in range(c.Hk):
+                bad = torch.rand(D // 16, generator=g) < .4
+                scales[page, h, s, bad] = 0x7F if t % 2 else 0xFF
+                safe[page, h, s, bad] = 0
+                for n in range(nn):
+                    if t < ctx - nn + 1 + n:
+                        nan[b, n, h * (c.H // c.Hk):(h + 1) * (c.H // c.Hk)] |= bad.repeat_interleave(16)
+    assert nan.any() and not nan[:, 0].any()
+    poisoned, c.v = c.v, clean
+    want = c.reference()
+    c.v = poisoned
+    out, lse = c.call(c.gpu(), ctas, with_lse=True)
+    assert torch.equal(out.isnan().cpu(), nan)
+    got = torch.where(nan.cuda(), torch.from_numpy(want[0]).cuda().to(out.dtype), out)
+    ref.check_attention(got, lse, want, int(c.ctx.max()), c.dtype)
+
+
 @gpu
 def test_strided_q_own_buffers_and_a_poisoned_workspace():
     c = Case([700, 0, 290], 2, 12, 2, 128, 64, seed=64)
