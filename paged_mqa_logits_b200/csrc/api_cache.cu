@@ -9,8 +9,6 @@
 namespace mqa {
 namespace {
 
-constexpr int kMaxBatch = 32768;
-
 int log2_of(int x) {
     int s = 0;
     while ((1 << s) < x) ++s;

@@ -10,6 +10,8 @@
 
 namespace mqa {
 
+constexpr int kMaxBatch = 32768;  // of the attention and the page calls
+
 // Where a kernel reports: the library's word (never NULL) and the caller's (may be).
 struct StatusWords {
     uint32_t* lib;

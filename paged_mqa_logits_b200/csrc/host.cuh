@@ -24,7 +24,8 @@ inline bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 constexpr int kMaxCtas = 4096;  // of a schedule
 
 // Raises a kernel's dynamic shared memory limit to `smem` on the current device
-// (asked of the runtime only once per device and kernel: `done` is the caller's).
+// (asked of the runtime only once per device and kernel: `done` is the caller's). Every call
+// for a kernel gives the same `smem`, so that calls on several host threads agree.
 template <typename Kernel>
 inline cudaError_t allow_smem(Kernel kernel, int device, uint32_t smem, uint32_t (&done)[64]) {
     if (device < 0 || device >= 64 || done[device] < smem) {

@@ -415,13 +415,16 @@ cudaError_t launch_fork(const int32_t* table, const int32_t* lens, const int32_t
 cudaError_t launch_resize(int device, int32_t* table, int32_t* lens, const int32_t* new_lens,
                           int32_t* refs, int32_t* src, int32_t* dst, const PagesArgs& a,
                           void* stream, bool pdl) {
+    // the limit is always raised to the most that a batch can need: set to this call's need,
+    // a smaller call on another host thread could lower it between the two
+    constexpr uint32_t kMostCached = 200000, kMost = (kMaxBatch + 1) * 4;
     static uint32_t done[2][64];
     const uint32_t pre = (uint32_t)(a.batch + 1) * 4;
-    const bool cached = pre * 2 <= 200000;
+    const bool cached = pre * 2 <= kMostCached;
     const uint32_t smem = cached ? pre * 2 : pre;
     if (smem > 40000) {
-        const cudaError_t e = cached ? allow_smem(resize_kernel<true>, device, smem, done[1])
-                                     : allow_smem(resize_kernel<false>, device, smem, done[0]);
+        const cudaError_t e = cached ? allow_smem(resize_kernel<true>, device, kMostCached, done[1])
+                                     : allow_smem(resize_kernel<false>, device, kMost, done[0]);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(cached ? resize_kernel<true> : resize_kernel<false>, dim3(1),

@@ -1,5 +1,7 @@
 """Page operations against a plain model that takes one row after the other."""
 import ctypes
+import shutil
+import threading
 
 import numpy as np
 import pytest
@@ -235,6 +237,33 @@ def test_unaligned_counts_and_a_captured_step():
         cells[cdst[:k]] = cells[csrc[:k]]
         same((*out, r), (ct, rl, cr))
         np.testing.assert_array_equal(cache.cpu().numpy(), cells)
+
+
+@gpu
+def test_resize_of_large_batches_on_several_host_threads(tmp_path):
+    """Batches whose shared memory is above the default, for the first time on every thread
+    at once (a fresh copy of the library each round: what it has set up is its own)."""
+    sizes, errors = (6000, 24000, 9000, 16000, 32768, 20000), []
+    keep = [dev(*[np.zeros(B)] * 3, np.zeros(4), *[np.zeros(B)] * 2) for B in sizes]
+    buffers = [[t.data_ptr() for t in tensors] for tensors in keep]
+    for i in range(4):
+        lib = ctypes.CDLL(shutil.copy(mq.library_path(), tmp_path / f"{i}.so"))
+        lib.mqa_pages_resize.argtypes = mq.library().mqa_pages_resize.argtypes
+        go = threading.Barrier(len(sizes))
+
+        def work(B, at):
+            p = params(batch=B, out_batch=0, max_pages_per_row=1, num_pages=4)
+            go.wait()
+            for _ in range(20):
+                errors.append(lib.mqa_pages_resize(*at, ctypes.byref(p), None))
+
+        threads = [threading.Thread(target=work, args=x) for x in zip(sizes, buffers)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+    assert len(errors) == 4 * 20 * len(sizes) and not any(errors)
 
 
 @gpu
