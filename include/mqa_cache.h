@@ -34,10 +34,10 @@ extern "C" {
 /* ------------------------------------------------------------ attention */
 
 typedef struct mqa_attention_params {
-    int32_t batch;              /* B >= 0 */
+    int32_t batch;              /* B, 0..32768 */
     int32_t next_n;             /* query positions per row, 1..4 */
     int32_t num_heads;          /* H query heads */
-    int32_t num_kv_heads;       /* Hk, divides H; H / Hk * next_n <= 128 */
+    int32_t num_kv_heads;       /* Hk <= 4096, divides H; H / Hk * next_n <= 128 (topk > 0: H / Hk <= 128) */
     int32_t head_dim;           /* D: 64 or 128 */
     int32_t page_size;          /* a power of two, 16..256 */
     int32_t num_pages;          /* pages in each of k_cache and v_cache */

@@ -63,10 +63,11 @@ int check_attention(const mqa_attention_params* p) {
     if (p->num_heads < 1 || p->num_kv_heads < 1 || p->num_heads % p->num_kv_heads)
         return fail(MQA_ERR_INVALID_ARG, "num_kv_heads must divide num_heads (got %d, %d)",
                     p->num_kv_heads, p->num_heads);
-    if (p->num_heads / p->num_kv_heads * (int64_t)p->next_n > 128 || p->num_kv_heads > 4096)
+    // the rows that share a tile: all positions' of a kv head, or (lists) one position's
+    if (p->num_heads / p->num_kv_heads * (int64_t)(p->topk > 0 ? 1 : p->next_n) > 128 || p->num_kv_heads > 4096)
         return fail(MQA_ERR_UNSUPPORTED,
-                    "num_heads / num_kv_heads * next_n must be <= 128 and num_kv_heads <= 4096 "
-                    "(got %d / %d * %d)", p->num_heads, p->num_kv_heads, p->next_n);
+                    "num_heads / num_kv_heads * next_n (lists: without next_n) must be <= 128 and "
+                    "num_kv_heads <= 4096 (got %d / %d * %d)", p->num_heads, p->num_kv_heads, p->next_n);
     if (p->head_dim != 64 && p->head_dim != 128)
         return fail(MQA_ERR_UNSUPPORTED, "head_dim must be 64 or 128 (got %d)", p->head_dim);
     if (p->dtype != MQA_DTYPE_BF16 && p->dtype != MQA_DTYPE_F16)

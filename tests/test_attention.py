@@ -189,6 +189,14 @@ def test_many_rows_heads_and_lists(case):
 
 
 @gpu
+@pytest.mark.parametrize("nn,Hk,D,dtype", [(2, 1, 128, "bf16"), (3, 1, 64, "bf16"), (4, 2, 64, "f16")])
+def test_lists_of_128_heads_and_several_positions(nn, Hk, D, dtype):
+    """A list's tile holds one position's heads, whatever the number of positions."""
+    Case([300, 1, 90, 0], nn, 128 * Hk, Hk, D, 64, dtype, seed=98 + nn, k=140).run_and_check()
+    Case([1500], nn, 128 * Hk, Hk, D, 64, dtype, seed=98 + nn, k=1025).run_and_check()
+
+
+@gpu
 def test_lists_with_holes_repeats_and_tokens_out_of_sight():
     """-1 anywhere, tokens at and past the context, negatives, a token twice, and a
     position whose list is empty."""
@@ -542,6 +550,16 @@ def test_lengths_that_would_wrap(kw):
     assert lib.paged_mqa_attention_fp4(16, 16, 16, 16, 16, 16, 16, 16, None, 16, ctypes.byref(p), None) == -4
     assert "2147418112" in lib.mqa_logits_last_error().decode()
     assert lib.mqa_attention_workspace_size(ctypes.byref(p), ctypes.byref(size)) == -4
+
+
+def test_rows_of_a_tile():
+    """128 at most: all positions' heads on a kv head, or with lists one position's."""
+    import ctypes
+    lib, size = mq.library(), ctypes.c_uint64(0)
+    for k, heads, n, fits in ((0, 64, 2, True), (0, 128, 2, False), (9, 128, 4, True), (9, 130, 1, False)):
+        p = params(topk=k, num_heads=heads, next_n=n, num_kv_heads=1)
+        rc = lib.mqa_attention_workspace_size(ctypes.byref(p), ctypes.byref(size))
+        assert (rc == -4) == (not fits), (k, heads, n)  # without a GPU what fits stops at the device
 
 
 def test_bad_pointers():
