@@ -91,8 +91,9 @@ int paged_mqa_attention_fp4(const void* q, const void* k_cache, const void* v_ca
                             float* lse, void* workspace, const mqa_attention_params* params,
                             void* stream);
 
-/* Bytes of workspace that a call with these params needs on the current device
- * (HOST *bytes; workspace_bytes, strides, status and flags are not looked at). */
+/* Bytes of workspace that a call with these params, or with a smaller batch or
+ * next_n, needs on the current device (HOST *bytes; workspace_bytes, strides,
+ * status and flags are not looked at). */
 int mqa_attention_workspace_size(const mqa_attention_params* params, uint64_t* bytes);
 
 /* ------------------------------------------------------------ appending */

@@ -183,7 +183,8 @@ def mqa_attention_workspace(q: torch.Tensor, *, kv_heads: int = 1, topk: int = 0
                             num_ctas: Optional[int] = None) -> torch.Tensor:
     """Workspace (uint8) for paged_mqa_attention_fp4 with this q [B, next_n, H, D],
     a schedule of num_ctas CTAs (None: the device's SMs) or token lists of length
-    topk. One serves every layer and step, but not two calls at the same time."""
+    topk. One serves every layer and step with no more rows and positions than q's, but
+    not two calls at the same time."""
     if q.dim() != 4:
         raise ValueError("q must be [B, next_n, H, D]")
     if _elsewhere(q, None):

@@ -125,10 +125,20 @@ int mqa_attention_workspace_size(const mqa_attention_params* params, uint64_t* b
     int dev = 0;
     rc = check_arch(&dev);
     if (rc != MQA_OK) return rc;
+    // one row and position: the lists that are cut into most parts
+    mqa_attention_params one = *params;
+    if (one.topk > 0) one.batch = one.next_n = 1;
     AttentionArgs a{};
-    rc = split_of(params, dev, a);
+    rc = split_of(&one, dev, a);
     if (rc != MQA_OK) return rc;
-    *bytes = workspace_of(a, params->head_dim);
+    *bytes = workspace_of(a, one.head_dim);
+    if (a.splits > 1) {  // any number of lists has no more parts than SMs (split_list)
+        int sms = 0;
+        rc = sm_count(dev, &sms);
+        if (rc != MQA_OK) return rc;
+        a.splits = sms / a.kv_heads;
+        *bytes = workspace_of(a, one.head_dim);
+    }
     return MQA_OK;
 }
 

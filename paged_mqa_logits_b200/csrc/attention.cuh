@@ -48,6 +48,8 @@ struct AttentionArgs {
 //   8.2 -> 7.1 us).
 // - In between, large CTAs, one an SM, with 256 tokens or more (128 lists of 2048: 21 us;
 //   28 with 4 small ones).
+// Where lists are split, all parts together are no more than the SMs: so much workspace
+// serves any number of lists.
 struct ListSplit { int splits; bool small; };
 inline ListSplit split_list(int64_t lists, int topk, int rows, int head_dim, int sms) {
     const bool narrow = rows <= 16;

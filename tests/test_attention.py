@@ -511,6 +511,20 @@ def test_position_of_the_split_changes_nothing_but_rounding():
         c.check(out, lse)
 
 
+@gpu
+@pytest.mark.parametrize("k", [None, 129, 300, 777, 2048])
+@pytest.mark.parametrize("heads,Hk,D", [(8, 1, 128), (21, 3, 64), (40, 1, 128)])
+def test_a_workspace_serves_smaller_batches_and_fewer_positions(k, heads, Hk, D):
+    """Its size never falls with the batch or the positions; one of a large batch serves a call of one row."""
+    size = np.array([[mq.mqa_attention_workspace(torch.empty(B, n, heads, D, dtype=torch.float16, device="cuda"),
+                                                 kv_heads=Hk, topk=k or 0).numel()
+                      for B in (1, 2, 3, 5, 8, 13, 30, 70, 74, 75, 148, 149, 400)] for n in (1, 2, 3)])
+    assert (np.diff(size, axis=0) >= 0).all() and (np.diff(size, axis=1) >= 0).all()
+    c = Case([800], 2, heads, Hk, D, 64, seed=99, k=k)
+    work = mq.mqa_attention_workspace(torch.empty(400, 3, heads, D, dtype=torch.float16, device="cuda"), kv_heads=Hk, topk=k or 0)
+    c.check(c.call(c.gpu(), workspace=work))
+
+
 # ---------------------------------------------------------------- refusals (CPU)
 def params(**kw):
     base = dict(batch=2, next_n=1, num_heads=8, num_kv_heads=2, head_dim=128, page_size=64,
