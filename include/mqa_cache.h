@@ -137,7 +137,8 @@ typedef struct mqa_append_params {
  *
  * values, k_values, v_values: NULL, or device [T][Hk][D] contiguous of the
  * tokens' type: what the cache now holds for each written token (exact in bf16,
- * rounded to f16 where that is too narrow); other tokens' rows are left.
+ * rounded to f16 where that is too narrow); other tokens' rows are left. Caches and
+ * values are buffers of their own.
  * Tokens are expected finite.
  */
 int mqa_cache_append_fp8(const void* x, void* kv_cache, const int32_t* block_table,
@@ -154,7 +155,8 @@ int mqa_cache_append_fp4(const void* k, const void* v, void* k_cache, void* v_ca
  * free page. Row b's pages are block_table[b][0 .. ceil(len_b / page_size) - 1],
  * lengths are clamped to [0, max_pages_per_row * page_size]. Table entries
  * outside [0, num_pages) are skipped (validate mode: MQA_STATUS_BAD_PAGE).
- * Results do not depend on the order in which threads run. */
+ * What a call writes may overlap none of its other buffers. Results do not
+ * depend on the order in which threads run. */
 
 typedef struct mqa_pages_params {
     int32_t batch;              /* rows of block_table, 0..32768 */
@@ -172,7 +174,6 @@ typedef struct mqa_pages_params {
  * out_table [out_batch][max_pages_per_row] (-1 behind a row's pages) and out_lens
  * [out_batch] whole, and counts page_refs from the old table's references to the
  * new one's: what no row goes on from is freed. parents device int32 [out_batch].
- * The outputs must not overlap the inputs.
  */
 int mqa_pages_fork(const int32_t* block_table, const int32_t* context_lens,
                    const int32_t* parents, int32_t* page_refs, int32_t* out_table,

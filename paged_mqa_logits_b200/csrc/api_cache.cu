@@ -52,6 +52,26 @@ int check_pool(int batch, int page_size, int ps_min, int num_pages, int max_page
     return MQA_OK;
 }
 
+// A buffer of a call: NULL or no bytes overlap nothing.
+struct Buffer {
+    const void* at;
+    int64_t bytes;
+};
+
+bool overlap(const Buffer& a, const Buffer& b) {
+    const char *x = static_cast<const char*>(a.at), *y = static_cast<const char*>(b.at);
+    return x && y && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether one of the first `written` buffers overlaps any other.
+template <int N>
+bool any_overlap(const Buffer (&all)[N], int written) {
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (overlap(all[i], all[j])) return true;
+    return false;
+}
+
 constexpr int kMostTokens = INT32_MAX - 65535;  // of a row, or of a token list
 
 int check_attention(const mqa_attention_params* p) {
@@ -248,8 +268,13 @@ static int run_append(bool fp8, const void* k, const void* v, void* k_cache, voi
         return fail(MQA_ERR_INVALID_ARG, "int32 buffers must be 4-byte aligned");
     if (p.k_stride_t % 8 || p.k_stride_h % 8 || (v && (p.v_stride_t % 8 || p.v_stride_h % 8)))
         return fail(MQA_ERR_INVALID_ARG, "the tokens' strides must be multiples of 8 elements");
-    if (v && v_cache == k_cache)
+    const int64_t cache = (int64_t)p.num_pages * p.page_size * p.num_kv_heads * (fp8 ? D + 4 : D / 2 + D / 16);
+    if (overlap({k_cache, cache}, {v_cache, cache}))
         return fail(MQA_ERR_INVALID_ARG, "k_cache and v_cache must be two buffers");
+    const int64_t values = (int64_t)p.num_tokens * p.num_kv_heads * D * 2;
+    const Buffer all[] = {{k_values, values}, {v_values, values}, {k_cache, cache}, {v_cache, cache}};
+    if (any_overlap(all, 2))
+        return fail(MQA_ERR_INVALID_ARG, "values must overlap neither each other nor the caches");
     uint32_t* lib_status = nullptr;
     rc = check_arch(nullptr, &lib_status);
     if (rc != MQA_OK) return rc;
@@ -320,11 +345,6 @@ static mqa::PagesArgs pages_args(const mqa_pages_params& p, uint32_t* lib_status
     return a;
 }
 
-static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
 int mqa_pages_fork(const int32_t* block_table, const int32_t* context_lens,
                    const int32_t* parents, int32_t* page_refs, int32_t* out_table,
                    int32_t* out_lens, const mqa_pages_params* params, void* stream) {
@@ -339,11 +359,11 @@ int mqa_pages_fork(const int32_t* block_table, const int32_t* context_lens,
     if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(parents, 4) ||
         !aligned(page_refs, 4) || !aligned(out_table, 4) || !aligned(out_lens, 4))
         return fail(MQA_ERR_INVALID_ARG, "int32 buffers must be 4-byte aligned");
-    const int64_t t = 4ll * p.batch * p.max_pages_per_row, l = 4ll * p.batch;
-    const int64_t ot = 4ll * p.out_batch * p.max_pages_per_row, ol = 4ll * p.out_batch;
-    if (overlap(block_table, t, out_table, ot) || overlap(context_lens, l, out_lens, ol) ||
-        overlap(parents, ol, out_lens, ol) || overlap(parents, ol, out_table, ot))
-        return fail(MQA_ERR_INVALID_ARG, "out_table and out_lens must not overlap the inputs");
+    const int64_t row = 4ll * p.max_pages_per_row;
+    const Buffer all[] = {{out_table, row * p.out_batch}, {out_lens, 4ll * p.out_batch}, {page_refs, 4ll * p.num_pages},
+                          {block_table, row * p.batch}, {context_lens, 4ll * p.batch}, {parents, 4ll * p.out_batch}};
+    if (any_overlap(all, 3))
+        return fail(MQA_ERR_INVALID_ARG, "out_table, out_lens and page_refs must not overlap each other or the inputs");
     uint32_t* lib_status = nullptr;
     rc = check_arch(nullptr, &lib_status);
     if (rc != MQA_OK) return rc;
@@ -368,8 +388,9 @@ int mqa_pages_resize(int32_t* block_table, int32_t* context_lens, const int32_t*
         !aligned(page_refs, 4) || !aligned(copy_src, 4) || !aligned(copy_dst, 4))
         return fail(MQA_ERR_INVALID_ARG, "int32 buffers must be 4-byte aligned");
     const int64_t l = 4ll * p.batch;
-    if (overlap(copy_src, l, copy_dst, l) || overlap(context_lens, l, new_lens, l))
-        return fail(MQA_ERR_INVALID_ARG, "context_lens, new_lens, copy_src and copy_dst must not overlap");
+    const Buffer all[] = {{block_table, l * p.max_pages_per_row}, {context_lens, l}, {page_refs, 4ll * p.num_pages},
+                          {copy_src, l}, {copy_dst, l}, {new_lens, l}};
+    if (any_overlap(all, 5)) return fail(MQA_ERR_INVALID_ARG, "the buffers must not overlap");
     int dev = 0;
     uint32_t* lib_status = nullptr;
     rc = check_arch(&dev, &lib_status);
@@ -395,6 +416,10 @@ int mqa_pages_compact(int32_t* block_table, const int32_t* context_lens, int32_t
     if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(page_refs, 4) ||
         !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(count, 4) || !aligned(page_map, 4))
         return fail(MQA_ERR_INVALID_ARG, "int32 buffers must be 4-byte aligned");
+    const int64_t l = 4ll * p.batch, half = p.num_pages / 2 * 4ll;
+    const Buffer all[] = {{block_table, l * p.max_pages_per_row}, {page_refs, 4ll * p.num_pages}, {copy_src, half},
+                          {copy_dst, half}, {count, 4}, {page_map, 4ll * p.num_pages}, {context_lens, l}};
+    if (any_overlap(all, 6)) return fail(MQA_ERR_INVALID_ARG, "the buffers must not overlap");
     uint32_t* lib_status = nullptr;
     rc = check_arch(nullptr, &lib_status);
     if (rc != MQA_OK) return rc;

@@ -333,6 +333,20 @@ def test_bad_pointers_and_pairs():
     assert ctypes.sizeof(mq.AppendParams) == 80 and mq.AppendParams.k_stride_t.offset == 40
 
 
+def test_overlapping_buffers():
+    """Caches of 4 pages of 4608 bytes and values of 1024: overlapping by 16 bytes, refused."""
+    lib, p = mq.library(), params()
+    size = dict(kc=4 * 64 * 72, vc=4 * 64 * 72, kv=4 * 128 * 2, vv=4 * 128 * 2)
+    good = dict(k=1 << 20, v=2 << 20, kc=3 << 20, vc=4 << 20, kv=5 << 20, vv=6 << 20)
+    for x in size:
+        for y in size:
+            for at in () if x == y else (good[y], good[y] + size[y] - 16, good[y] - size[x] + 16):
+                b = {**good, x: at}
+                assert lib.mqa_cache_append_fp4(b["k"], b["v"], b["kc"], b["vc"], 16, 16, 16, b["kv"], b["vv"], ctypes.byref(p), None) == -1
+                error = lib.mqa_logits_last_error().decode()
+                assert "two buffers" in error if {x, y} == {"kc", "vc"} else "overlap" in error, (x, y, error)
+
+
 def test_binding_checks_shapes():
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     k = x[:, None]

@@ -331,6 +331,25 @@ def test_bad_pointers():
     assert ctypes.sizeof(mq.PagesParams) == 32
 
 
+def test_overlapping_buffers():
+    """Every buffer that a call writes, against each of its others: overlapping by an entry, refused."""
+    lib, p = mq.library(), params()  # tables of 32 bytes, lengths of 8, counts and maps of 32, lists of 16
+    a = [i << 20 for i in range(1, 8)]
+    size = dict(table=32, lens=8, refs=32, half=16, one=4)
+    calls = ((lib.mqa_pages_fork, ("table", "lens", "lens", "refs", "table", "lens"), (3, 4, 5)),
+             (lib.mqa_pages_resize, ("table", "lens", "lens", "refs", "lens", "lens"), (0, 1, 3, 4, 5)),
+             (lib.mqa_pages_compact, ("table", "lens", "refs", "half", "half", "one", "refs"), (0, 2, 3, 4, 5, 6)))
+    for fn, kinds, written in calls:
+        for i in written:
+            for j in range(len(kinds)):
+                if i == j:
+                    continue
+                for at in (a[j], a[j] + size[kinds[j]] - 4, a[j] - size[kinds[i]] + 4):
+                    args = a[:len(kinds)]
+                    args[i] = at
+                    assert fn(*args, ctypes.byref(p), None) == -1 and "overlap" in lib.mqa_logits_last_error().decode()
+
+
 def test_copy_refusals():
     lib, p = mq.library(), ctypes.byref(params())
 
