@@ -212,8 +212,8 @@ int mqa_pages_compact(int32_t* block_table, const int32_t* context_lens, int32_t
  * Copies pages src[i] -> dst[i], i < n, in each of num_caches pools: caches is a
  * HOST array of device pointers (16-byte aligned), page_bytes a HOST array of
  * their pages' sizes (multiples of 16). count: NULL, or device int32: only
- * i < *count. Pairs with either outside [0, num_pages) are skipped (-1 silently,
- * others raise MQA_STATUS_BAD_PAGE in validate mode). A page must not be a
+ * i < *count. Pairs with either outside [0, num_pages) are skipped (where that is -1
+ * silently, other numbers raise MQA_STATUS_BAD_PAGE in validate mode). A page must not be a
  * destination twice, nor source and destination in one call. params: num_pages,
  * flags and status are looked at.
  */

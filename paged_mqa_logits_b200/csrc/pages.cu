@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
                 for (int k = 0; k < 4; ++k)
                     if (c + 32 * k < chunks) __stcs(to + c + 32 * k, v[k]);
             }
-        } else if ((s != -1 || d != -1) && lane == 0) {
+        } else if (lane == 0 && (s < -1 || s >= a.num_pages || d < -1 || d >= a.num_pages)) {
             report_checked(a.status, MQA_STATUS_BAD_PAGE);
         }
         i = next;

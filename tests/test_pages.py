@@ -198,6 +198,19 @@ def test_bad_entries_are_skipped_and_reported():
 
 
 @gpu
+def test_copies_of_no_page():
+    """-1 on either side skips the pair without a word; other numbers outside the pool are named."""
+    cache = torch.randint(0, 256, (4, 64), dtype=torch.uint8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for s, d, bits in ((-1, -1, 0), (-1, 2, 0), (2, -1, 0), (-1, 9, mq.MQA_STATUS_BAD_PAGE), (-2, 1, mq.MQA_STATUS_BAD_PAGE),
+                       (4, -1, mq.MQA_STATUS_BAD_PAGE)):
+        got = cache.cuda()
+        mq.mqa_pages_copy(got, *dev([s], [d]), flags=mq.MQA_FLAG_VALIDATE, status=status.zero_())
+        assert int(status) == bits and torch.equal(got.cpu(), cache), (s, d)
+    mq.mqa_logits_clear_status()
+
+
+@gpu
 def test_unaligned_counts_and_a_captured_step():
     """page_refs as a view that starts off a 16-byte boundary; fork, resize, copy and
     compact captured once and replayed on other lengths."""
