@@ -198,6 +198,21 @@ def test_even_rows_strides_and_keys_alone():
 
 
 @gpu
+@pytest.mark.parametrize("D,dtype", [(32, "bf16"), (64, "f16"), (128, "bf16")])
+def test_even_rows_fp8(D, dtype):
+    """No offsets, a strided slice; rows whose first new tokens have no place."""
+    ctx, ps = [5, 3, 40, 0, 1], 8
+    table, P = setup(ctx, ps, seed=1)
+    x = tokens((15, 2, D), TYPES[dtype], seed=2)
+    cache = torch.randint(0, 256, (P, ps * (D + 4)), generator=torch.Generator().manual_seed(3), dtype=torch.uint8)
+    dc = cache.cuda()
+    assert mq.mqa_cache_append_fp8(x.cuda()[:, 1], dc, table.cuda(), torch.tensor(ctx, dtype=torch.int32, device="cuda")) is None
+    where = places(table, ctx, None, 15, ps, P, per_row=3)
+    assert where.count(None) == 3 + 2
+    np.testing.assert_array_equal(dc.cpu().numpy(), expected_fp8(cache.numpy(), x[:, 1], where, ps)[0])
+
+
+@gpu
 @pytest.mark.parametrize("fp8", [False, True])
 def test_tokens_without_a_place_are_not_written(fp8):
     """Positions before the row's start and behind its table, bad pages, lengths of 0:

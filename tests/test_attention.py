@@ -238,6 +238,72 @@ def test_scores_that_rise_along_the_row():
     c.run_and_check()
 
 
+LONG = [
+    ([131072, 40001], 1, 8, 1, 128, 64, "bf16", None, None),
+    ([100003], 1, 32, 2, 64, 256, "f16", 3, None),
+    ([65537, 0, 5], 3, 10, 2, 128, 16, "bf16", 1, None),
+    ([131072], 2, 64, 1, 128, 64, "bf16", 1, None),
+    ([70000, 131071, 33], 4, 32, 1, 64, 16, "f16", None, None),
+    ([50001], 1, 20, 1, 128, 128, "bf16", 7, None),
+    ([131072, 9], 1, 8, 1, 128, 64, "f16", None, 60000),
+    ([131072], 2, 40, 1, 64, 64, "bf16", None, 50001),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", LONG, ids=[f"{c[0][0]}-n{c[1]}-h{c[2]}.{c[3]}-d{c[4]}-s{c[7]}-k{c[8]}" for c in LONG])
+def test_long_rows(case):
+    """Rows of tens of thousands of tokens, also in one CTA, with scores that rise along them."""
+    ctx, nn, H, Hk, D, ps, dtype, ctas, k = case
+    c = Case([1], nn, H, Hk, D, ps, dtype)
+    g = torch.Generator(device="cuda").manual_seed(140 + LONG.index(case))
+    B, P, W = len(ctx), sum(-(-n // ps) for n in ctx) + 2, -(-max(ctx) // ps)
+    random = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g, device="cuda")  # noqa: E731
+    order, at = torch.randperm(P, generator=g, device="cuda").to(torch.int32), 0
+    d = {"table": torch.full((B, W), -1, dtype=torch.int32, device="cuda"),
+         "ctx": torch.tensor(ctx, dtype=torch.int32, device="cuda"), "indices": None,
+         "q": (2 * torch.randn(B, nn, H, D, generator=g, device="cuda")).to(c.dtype)}
+    for n in "kv":
+        d[n] = random(0, 256, P, Hk * ps * (D // 2 + D // 16)).to(torch.uint8)
+        c.split(d[n])[1].copy_(random(0x28, 0x38, P, Hk, ps, D // 16))  # 0.25 to 0.9
+    for b, n in enumerate(ctx):
+        pages = order[at:at + -(-n // ps)]
+        d["table"][b, :len(pages)] = pages
+        at += len(pages)
+        if n > 100:  # K grows along the row, to four times
+            by = 16 * torch.arange(len(pages), device="cuda") // len(pages)
+            c.split(d["k"])[1][pages.long()] += by[:, None, None, None].to(torch.uint8)
+    if k:
+        c.indices = d["indices"] = torch.stack([torch.stack([random(-2, max(n, 1), k) for _ in range(nn)]) for n in ctx]).to(torch.int32)
+    out, lse = c.call(d, ctas, with_lse=True)
+    table = torch.tensor([-1.0 if i >= 8 else 1.0 for i in range(16)], dtype=torch.float64, device="cuda") * \
+        torch.tensor(list(ref.E2M1) * 2, dtype=torch.float64, device="cuda")
+    scales = torch.tensor(ref.E4M3, dtype=torch.float64, device="cuda")
+    want = [torch.zeros(B, nn, H, D, dtype=torch.float64, device="cuda"), torch.full((B, nn, H), -np.inf, dtype=torch.float64, device="cuda"),
+            torch.zeros(B, nn, H, D, dtype=torch.float64, device="cuda"), torch.zeros(B, nn, H, dtype=torch.float64, device="cuda")]
+    for b, n in enumerate(ctx):
+        for i in range(nn):
+            upto = max(n - nn + 1 + i, 0)
+            t = torch.arange(upto, device="cuda")
+            if k:
+                t = d["indices"][b, i].long()
+                t = t[(t >= 0) & (t < upto)]
+            if not len(t):
+                continue
+            for h in range(Hk):
+                kv = []
+                for m in "kv":
+                    codes, sc = (x[d["table"][b, t // ps].long(), h, t % ps] for x in c.split(d[m]))
+                    both = torch.stack((codes & 15, codes >> 4), -1).flatten(1)
+                    kv.append(table[both.long()] * scales[sc.long()].repeat_interleave(16, 1))
+                qh = d["q"][b, i, h * (H // Hk):(h + 1) * (H // Hk)].double()
+                x = c.scale * qh @ kv[0].T
+                p, rows = torch.softmax(x, -1), (b, i, slice(h * (H // Hk), (h + 1) * (H // Hk)))
+                want[0][rows], want[1][rows], want[2][rows] = p @ kv[1], torch.logsumexp(x, -1), p @ kv[1].abs()
+                want[3][rows] = c.scale * (qh.abs() @ kv[0].abs().T).amax(-1) * 2.0 ** -16
+    ref.check_attention(out, lse, [w.cpu().numpy() for w in want], max(ctx), c.dtype)
+
+
 @gpu
 @pytest.mark.parametrize("at", [0, 20000])
 @pytest.mark.parametrize("heads", [8, 12, 32, 64, 128])

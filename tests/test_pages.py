@@ -98,6 +98,26 @@ def test_resize(B, W, ps, P, seed):
 
 
 @gpu
+@pytest.mark.parametrize("B,dry", [(24999, False), (25000, False), (25000, True), (32768, True)])
+def test_resize_of_large_batches(B, dry):
+    """Around the batch from which on a row's place is found again, with and without enough pages."""
+    rng = np.random.default_rng(B + dry)
+    ps, W = 16, 3
+    table, lens, refs = pool(rng, B, W, ps, 3 * B)
+    new = rng.integers(0, W * ps + 1, B)
+    if dry:
+        free = np.flatnonzero(refs == 0)
+        refs[free[len(free) // 8:]] = 1
+    t, l, n, r = dev(table, lens, new, refs)
+    mq.mqa_logits_clear_status()
+    src, dst = mq.mqa_pages_resize(t, l, n, r, page_size=ps)
+    *want, ran_out = ref.resize(table, lens, new, refs, ps)
+    same((t, l, r, src, dst), want)
+    assert ran_out == dry and mq.mqa_logits_get_status() == (mq.MQA_STATUS_NO_PAGES if dry else 0)
+    mq.mqa_logits_clear_status()
+
+
+@gpu
 def test_resize_with_the_pool_just_enough_and_one_short():
     ps = 16
     for spare in (0, 1):
