@@ -51,8 +51,11 @@ constexpr float kMost = 65504.f;
 // Registers of a thread: at launch (what the compiler gives 640 threads; the launch checks
 // it), and of the roles' four-warp groups afterwards, which together take no more, so that
 // the softmax groups' request is met once the others have given theirs back (32 rows of
-// two positions and 64 heads, 32768 to 131072 tokens: 227 -> 222 us).
-constexpr int kRegsLaunch = 96, kRegsMma = 48, kRegsSoftmax = 152, kRegsDequant = 64;
+// two positions and 64 heads, 32768 to 131072 tokens: 227 -> 222 us). The walk, the copies
+// and the last tokens' scales do not fit 64 in the dequantising warps (5 rows of up to 79593
+// tokens, three positions of 48 heads on 8, D = 64: 104 us, 101.5 with 72); with 80, and 136
+// for the softmax, 128 lists of 2048 take 34.5 us for 28.2.
+constexpr int kRegsLaunch = 96, kRegsMma = 48, kRegsSoftmax = 144, kRegsDequant = 72;
 static_assert(kRegsMma + 2 * kRegsSoftmax + 2 * kRegsDequant <= kWideThreads / 128 * kRegsLaunch, "registers");
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 // TMEM columns: three S buffers of 128 (P over their second halves), O. With three, S
