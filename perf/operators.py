@@ -186,7 +186,7 @@ def prepare_attention(case, g):
         best, token = rank.topk(k, dim=-1, largest=False)
         token = torch.where(best < 2.0, token, wide).sort(-1).values
         s["list"] = torch.where(token < wide, token, -1).to(torch.int32)
-    if own:  # the split of the rows over the GPU and the partial results' memory, kept for all layers and steps
+    if own:  # the split of the rows over the GPU, kept for all layers of a step, and the partial results' memory, for all steps
         import paged_mqa_logits_b200 as mq
 
         s["plan"] = None if k else mq.mqa_logits_schedule(s["context"])
