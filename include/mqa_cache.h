@@ -62,14 +62,14 @@ typedef struct mqa_attention_params {
  * for the logits), or with topk > 0 the entries of indices[b][n] with
  * 0 <= t < ctx_bn; other entries (-1 among them) may stand anywhere in the list
  * and are skipped, and a token listed twice counts twice. A position that sees
- * no token gets out = 0 and lse = -inf. What lies in slots that are not visible
- * (NaN scales among it) never reaches a result.
+ * no token gets out = 0 and lse = -inf. What lies in slots that a position does
+ * not see (NaN scales among it) never reaches its result.
  *
  * q:            device bf16 or f16 [B][next_n][H][D] with the strides of params
  *               (D contiguous), 16-byte aligned. The kernels multiply in f16:
  *               a bf16 row (b, n, h) is first scaled by a power of two, undone
  *               on the scores, so it is exact down to 2^-31 of the row's largest.
- *               Finite values are expected.
+ *               Finite values are expected, and scores within +-2^26.
  * k_cache, v_cache: device bytes [num_pages][Hk][page_size * (D/2 + D/16)],
  *               16-byte aligned, FP4 pages; they may be the same buffer.
  * block_table, context_lens: as for paged_mqa_logits_fp4.

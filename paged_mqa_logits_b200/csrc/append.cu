@@ -4,7 +4,7 @@
 // token's 2 to 8 threads share their maximum by shuffles), so a token's bytes
 // are read once in 16-byte loads and written once in 8- or 16-byte stores.
 // Bound by memory: 48 thousand tokens of 8 heads, K and V, D = 128, with the values
-// (449 MB) take 82 us, 0.85 of the copy rate; 127 thousand FP8 keys (82 MB) 16 us, 0.79.
+// (449 MB) take 83 us, 0.84 of the copy rate; 127 thousand FP8 keys (82 MB) 16 us, 0.81.
 // One token each of 128 rows takes 2.7 us, a launch.
 #include <cuda_runtime.h>
 

@@ -19,10 +19,10 @@
 // attention_wide.cu. mma.sync runs one
 // m16n8k16 every two cycles an SM, which 8 rows need 2.1 of a token (D = 128, K and V)
 // and 32 rows 8.5, against 6.3 cycles that HBM needs to bring it: 32 rows, lists of
-// 2048 tokens, took 47 us here and 27 us there; one row of 1000 tokens 16.7 and 14.4.
+// 2048 tokens, took 47 us here and 28 us there; one row of 1000 tokens 16.7 and 14.4.
 //
 // Measured: 64 rows of 1024 to 8192 tokens, 8 kv heads with 8 query heads each, D =
-// 128: 88 us for 342 MB, 3.9 TB/s or 0.60 of the copy rate. What bounds it is issue: 63
+// 128: 89 us for 342 MB, 3.8 TB/s or 0.60 of the copy rate. What bounds it is issue: 63
 // % of the issue slots, the integer pipe (e2m1 conversions, nibbles) at 55 %, the
 // tensor pipe at 24 %, and 11 % of the time before the first and after the last
 // token. Rows of 16 query heads: 154 tokens a microsecond and SM, mma.sync at 0.7.

@@ -27,9 +27,9 @@
 // MQA_STATUS_TIMEOUT and every role leaves.
 //
 // Measured: 32 rows of 32768 to 131072 tokens, two positions of 64 heads, one kv head,
-// D = 128: 222 us for 380 MB and 172 GFLOP, 0.46 of the time that the products need at
-// the bf16 peak. What bounds it is latency: a tile's chain (dequantise, S, softmax, P,
-// O) takes longer than its 1.6 us share, with two tiles in each stage; leaving out any
+// D = 128: 240 us for 380 MB and 172 GFLOP; the products need 0.43 of that at the bf16
+// peak. What bounds it is latency: a tile's chain (dequantise, S, softmax, P,
+// O) takes longer than its 1.7 us share, with two tiles in each stage; leaving out any
 // one of its parts (the exponentials, the conversions, half of the products, the
 // copies) saves 10 to 20 %. A row of its own costs about 8 us besides: q, the first
 // tile's chain and the result do not overlap the row before.
