@@ -343,6 +343,42 @@ def test_a_sink_over_a_long_flat_row(listed, heads, at):
 
 
 @gpu
+@pytest.mark.parametrize("heads", [6, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_as_large_as_they_may_be(heads, sign):
+    """Scores of up to 2^26, all of one sign or both: where one token stands out by more than the
+    scores' error, its v is the result."""
+    c = Case([1000, 40], 1, heads, 1, 128, 64, seed=97)
+    codes, _ = c.split(c.k)
+    if sign < 0:
+        codes &= 0x77  # every k and q positive, the scale negative: every score is
+        c.q = c.q.abs()
+    c.scale = sign * 2.0 ** 22
+    K = ref.decode_fp4(c.k.numpy(), 1, 64, 128)
+    page = [c.table[b].numpy()[np.arange(n) // 64] for b, n in enumerate(c.ctx.tolist())]
+    k = [K[p, 0, np.arange(len(p)) % 64] for p in page]
+    top = max(np.abs(c.q[b, 0].double().numpy() @ x.T).max() for b, x in enumerate(k))
+    c.q = (c.q * (15.9 / top)).to(torch.bfloat16)
+    got, lse = c.call(c.gpu(), with_lse=True)
+    assert torch.isfinite(got).all() and torch.isfinite(lse).all()
+    V = ref.decode_fp4(c.v.numpy(), 1, 64, 128)
+    clear = 0
+    for b, p in enumerate(page):
+        x = c.scale * c.q[b, 0].double().numpy() @ k[b].T
+        assert np.abs(x).max() <= 2 ** 26
+        order = np.argsort(-x, axis=1)
+        err = abs(c.scale) * (np.abs(c.q[b, 0].double().numpy()) @ np.abs(k[b]).T).max(1) * 2.0 ** -16
+        for h in range(heads):
+            if x[h, order[h, 0]] - x[h, order[h, 1]] > 2 * err[h] + 100:
+                t = order[h, 0]
+                want = torch.from_numpy(V[p[t], 0, t % 64])
+                assert torch.allclose(got[b, 0, h].double().cpu(), want, rtol=2 ** -8, atol=0), (b, h)
+                assert abs(float(lse[b, 0, h]) - x[h, t]) <= err[h] + 2.0 ** -21 * abs(x[h, t])
+                clear += 1
+    assert clear >= heads
+
+
+@gpu
 @pytest.mark.parametrize("scale", [0.0, -0.125, 3.0])
 def test_scales(scale):
     c = Case([290, 31], 2, 6, 2, 64, 32, "f16", seed=63, q_gain=0.5)
@@ -361,6 +397,10 @@ NAN = [
     ([257, 600, 129, 3], 3, 20, 1, 64, 16, "bf16", 3),
     ([258, 514, 2], 4, 32, 1, 128, 64, "bf16", 2),
     ([130, 0, 257], 2, 40, 2, 64, 64, "f16", 1),
+    # many rows to a CTA
+    (many(40, 200, 31), 4, 24, 1, 128, 16, "bf16", 2),
+    (many(40, 140, 32), 3, 60, 2, 64, 16, "f16", 1),
+    (many(30, 300, 33), 2, 6, 1, 64, 16, "bf16", 1),
 ]
 
 
